@@ -129,6 +129,58 @@ typedef struct {
                            step that brings it to K folds them into the checkpoint */
 } ssd_replay_desc_t;
 
+/* Short causal convolution problem description. */
+typedef struct {
+    int64_t batch;      /* >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
+    int64_t seqlen;     /* >= 0; 0 writes final_state = init_state (or zeros); 1 for ssd_conv1d_update */
+    int64_t channels;   /* multiple of 8, <= 2^20 */
+    int64_t width;      /* taps: 2, 3 or 4 */
+    int64_t x_stride;   /* elements from a token's row of x to the next: >= channels, multiple of 8 */
+    int64_t dx_stride;  /* the same of dx (backward; ignored otherwise) */
+    int64_t split1;     /* channels of the second and the third output tensor: multiples of 8, 0 = */
+    int64_t split2;     /* no such tensor; the first one has the other channels (at least 8) */
+    int32_t io_dtype;   /* dtype of x (backward: also of dy) */
+    int32_t y_dtype;    /* dtype of the outputs (backward: of dx) */
+    int32_t state_dtype;/* dtype of the kept inputs */
+    int32_t activation; /* 0: none, 1: SiLU */
+} ssd_conv1d_desc_t;
+
+/* Selective scan problem description (a decay per channel and state). */
+typedef struct {
+    int64_t batch;      /* >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
+    int64_t seqlen;     /* >= 0; 0 writes final_state = init_state (or zeros); 1 for ssd_selective_state_update */
+    int64_t channels;   /* D; channels / ngroups is a multiple of 8; <= 2^20 */
+    int64_t dstate;     /* N, multiple of 8, <= 256 */
+    int64_t ngroups;    /* G >= 1: channel d uses group d / (D / G) of B and C */
+    int64_t z_stride;   /* elements from a token's row of the gate z to the next: >= channels,
+                           multiple of 8 (ignored without z); dz is dense */
+    int32_t io_dtype;   /* dtype of x, dt_raw, B, C, z (backward: also of dy) */
+    int32_t y_dtype;    /* dtype of y (backward: of the gradients of the io tensors) */
+    int32_t state_dtype;/* dtype of the states */
+} ssd_selective_desc_t;
+
+/* Group normalisation problem description. */
+typedef struct {
+    int64_t rows;       /* tokens: >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
+    int64_t channels;   /* <= 2^20 */
+    int64_t ngroups;    /* channels / ngroups is a multiple of 8, <= 16384 */
+    int64_t z_stride;   /* elements from a row of the gate z to the next: >= channels, multiple of 8
+                           (ignored without z); dz is dense */
+    float eps;          /* added to the variance: > 0 */
+    int32_t x_dtype;    /* dtype of x */
+    int32_t io_dtype;   /* dtype of z (backward: also of dy) */
+    int32_t y_dtype;    /* dtype of y (backward: of dx and dz) */
+    int32_t center;     /* 0: divided by the root of the mean square; 1: the group's mean subtracted first */
+    int32_t activation; /* ssd_norm_activation_t */
+} ssd_group_norm_desc_t;
+
+typedef enum {
+    SSD_NORM_NONE = 0,        /* y = v, v the normalised and weighted input; z is NULL */
+    SSD_NORM_SILU = 1,        /* y = silu(v); z is NULL */
+    SSD_NORM_GATE_AFTER = 2,  /* y = v silu(z) */
+    SSD_NORM_GATE_BEFORE = 3  /* y = v with x silu(z) normalised in the place of x */
+} ssd_norm_activation_t;
+
 /* Library version as MAJOR * 10000 + MINOR * 100 + PATCH. */
 int ssd_version(void);
 
@@ -476,6 +528,165 @@ ssd_status_t ssd_replay_buffer_size(const ssd_replay_desc_t* desc, size_t* bytes
 ssd_status_t ssd_replay_step(const ssd_replay_desc_t* desc, void* checkpoint, void* buffer, int32_t fill,
                              const void* x, const void* dt_raw, const float* dt_bias, const float* A,
                              const void* B, const void* C, const float* D, void* y, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The operators of a layer around and beside the scan.
+ *
+ * The parameters (weights, biases, A, D) are fp32 like the scan's; gradients
+ * follow its rule: dy has io_dtype, the gradients of the io tensors y_dtype.
+ * SiLU is silu(v) = v / (1 + exp(-v)).  These calls keep no state in the
+ * library and use no device memory but their arguments, so calls on different
+ * streams may overlap (backward calls: on different workspaces).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Short causal convolution along the tokens, one filter per channel, before
+ * the scan: with W taps, input token t of channel c
+ *   v_t = bias[c] + sum_{k < W} weight[c][k] x_{t-W+1+k},   y_t = v_t or silu(v_t)
+ * The W - 1 inputs before the first token are the kept ones of init_state.
+ * The channels go to up to three dense tensors, as the scan takes x, B and C.
+ *
+ *  x           [b][L] rows of x_stride, the first `channels` elements of each  io_dtype
+ *  weight      [channels][width] fp32   required;   bias [channels] fp32  nullable (= 0)
+ *  init_state  [b][width-1][channels] state_dtype, oldest first; nullable (= 0)
+ *  pad_left    [b] int32, nullable (= 0): as ssd_chunk_scan_fwd_varlen's.  The
+ *              tokens before it are absent, whatever x holds there: the sequence
+ *              starts at pad_left[b] from init_state[b]; y before it is written as 0
+ *  y0, y1, y2  [b][L][channels - split1 - split2], [b][L][split1], [b][L][split2]
+ *              y_dtype; y1 (y2) is NULL where split1 (split2) is 0
+ *  final_state [b][width-1][channels] state_dtype, nullable: the last width - 1
+ *              inputs, init_state's among them where there are fewer tokens
+ * No output may overlap an input or another output.
+ * Errors: SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_ALIGNMENT (nothing
+ * launched), SSD_ERR_CUDA.
+ */
+ssd_status_t ssd_conv1d_fwd(const ssd_conv1d_desc_t* desc, const void* x, const float* weight, const float* bias,
+                            const void* init_state, const int32_t* pad_left, void* y0, void* y1, void* y2,
+                            void* final_state, void* stream);
+
+/*
+ * One token of ssd_conv1d_fwd, in place on the kept inputs `state`
+ * [b][width-1][channels]; x has b rows of x_stride, y0, y1, y2 b rows.
+ * desc->seqlen is 1.  Errors: as ssd_conv1d_fwd.
+ */
+ssd_status_t ssd_conv1d_update(const ssd_conv1d_desc_t* desc, void* state, const void* x, const float* weight,
+                               const float* bias, void* y0, void* y1, void* y2, void* stream);
+
+/*
+ * Backward pass of ssd_conv1d_fwd (without pad_left): gradients of
+ * sum_t <dy_t, y_t> + <dfinal_state, final_state>.
+ *  dy0, dy1, dy2 as y0, y1, y2, io_dtype;  dfinal_state as final_state, nullable (= 0)
+ *  dx            [b][L] rows of dx_stride, y_dtype: the first `channels` elements of
+ *                each row are written, the rest is left as it was
+ *  dweight [channels][width], dbias [channels] (nullable) fp32: summed over
+ *                batch and tokens in a fixed order (no atomics)
+ *  dinit_state   [b][width-1][channels] state_dtype, nullable
+ *  workspace     >= ssd_conv1d_bwd_workspace_size bytes, 256-byte aligned, clobbered
+ * Errors: as ssd_conv1d_fwd, and SSD_ERR_WORKSPACE.
+ */
+ssd_status_t ssd_conv1d_bwd(const ssd_conv1d_desc_t* desc, const void* x, const float* weight, const float* bias,
+                            const void* init_state, const void* dy0, const void* dy1, const void* dy2,
+                            const void* dfinal_state, void* dx, float* dweight, float* dbias, void* dinit_state,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ssd_conv1d_bwd needs for `desc`.  Pure host function. */
+ssd_status_t ssd_conv1d_bwd_workspace_size(const ssd_conv1d_desc_t* desc, size_t* bytes);
+
+/*
+ * Selective scan: the recurrence with a decay for each channel and state
+ * instead of the chunked scan's one scalar per head.  Per batch b, channel d:
+ *   dt_t = softplus(dt_raw_t + dt_bias)
+ *   h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t x_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)        (no z: no factor)
+ *
+ *  x, dt_raw   [b][L][D] io_dtype;  dt_bias [D] fp32 nullable (= 0)
+ *  A           [D][N] fp32 (taken as given; A <= 0 is the intended use)
+ *  B, C        [b][L][G][N] io_dtype;  D [D] fp32 nullable (= 0)
+ *  z           [b][L] rows of z_stride, io_dtype, nullable
+ *  init_state  [b][D][N] state_dtype, nullable (= 0)
+ *  pad_left    [b] int32, nullable (= 0): tokens before it are absent, whatever the
+ *              inputs hold there (as ssd_conv1d_fwd's); y before it is written as 0
+ *  y           [b][L][D] y_dtype
+ *  final_state [b][D][N] state_dtype, nullable
+ *  workspace   >= ssd_selective_scan_workspace_size bytes (which may be 0: then
+ *              NULL is taken), 256-byte aligned, clobbered
+ * No output may overlap an input or another output.
+ * Errors: SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_ALIGNMENT,
+ * SSD_ERR_WORKSPACE (nothing launched), SSD_ERR_CUDA.
+ */
+ssd_status_t ssd_selective_scan_fwd(const ssd_selective_desc_t* desc, const void* x, const void* dt_raw,
+                                    const float* dt_bias, const float* A, const void* B, const void* C,
+                                    const float* D, const void* z, const void* init_state, const int32_t* pad_left,
+                                    void* y, void* final_state, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Workspace bytes ssd_selective_scan_fwd needs for `desc`.  Pure host function. */
+ssd_status_t ssd_selective_scan_workspace_size(const ssd_selective_desc_t* desc, size_t* bytes);
+
+/*
+ * One token of ssd_selective_scan_fwd, in place on `state` [b][D][N]
+ * (a bf16 state is rounded to nearest even; y reads it before that rounding):
+ * x, dt_raw, y [b][D], B, C [b][G][N], z b rows of z_stride.  desc->seqlen is 1.
+ * Errors: as ssd_selective_scan_fwd (no workspace).
+ */
+ssd_status_t ssd_selective_state_update(const ssd_selective_desc_t* desc, void* state, const void* x,
+                                        const void* dt_raw, const float* dt_bias, const float* A, const void* B,
+                                        const void* C, const float* D, const void* z, void* y, void* stream);
+
+/*
+ * Backward pass of ssd_selective_scan_fwd (without pad_left): gradients of
+ * sum_t <dy_t, y_t> + <dfinal_state, final_state> by every input.
+ *  dy [b][L][D] io_dtype;  dfinal_state [b][D][N] state_dtype, nullable (= 0)
+ *  dx, ddt_raw [b][L][D], dB, dC [b][L][G][N] (summed over a group's channels),
+ *  dz [b][L][D] (dense; required with z, NULL without) y_dtype
+ *  dA [D][N] fp32;  ddt_bias, dD [D] fp32, nullable;  dinit_state [b][D][N]
+ *  state_dtype, nullable.  Sums are formed in a fixed order (no atomics).
+ *  workspace  >= ssd_selective_scan_bwd_workspace_size bytes, 256-byte aligned
+ * Errors: as ssd_selective_scan_fwd.
+ */
+ssd_status_t ssd_selective_scan_bwd(const ssd_selective_desc_t* desc, const void* x, const void* dt_raw,
+                                    const float* dt_bias, const float* A, const void* B, const void* C,
+                                    const float* D, const void* z, const void* init_state, const void* dy,
+                                    const void* dfinal_state, void* dx, void* ddt_raw, float* ddt_bias, float* dA,
+                                    void* dB, void* dC, float* dD, void* dz, void* dinit_state, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ssd_selective_scan_bwd needs for `desc`.  Pure host function. */
+ssd_status_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_desc_t* desc, size_t* bytes);
+
+/*
+ * Group normalisation of rows of channels (channels last) with an activation,
+ * as a layer applies it to the scan's output.  Statistics are of one row and
+ * one group of channels / ngroups neighbouring channels, so that a token's
+ * result depends on no other token.  With u = x (or x silu(z), see the
+ * activations of ssd_norm_activation_t), m the group's mean (0 unless center):
+ *   v = (u - m) / sqrt(mean((u - m)^2) + eps) * weight + bias
+ *  x       [rows][channels] x_dtype;  z rows of z_stride, io_dtype: required for
+ *          the two gates, NULL otherwise
+ *  weight, bias [channels] fp32, nullable (= 1, = 0);  y [rows][channels] y_dtype
+ * y may not overlap an input.
+ * Errors: SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_ALIGNMENT (nothing
+ * launched), SSD_ERR_CUDA.
+ */
+ssd_status_t ssd_group_norm_fwd(const ssd_group_norm_desc_t* desc, const void* x, const void* z, const float* weight,
+                                const float* bias, void* y, void* stream);
+
+/*
+ * Backward pass of ssd_group_norm_fwd (the statistics are formed again).
+ *  dy [rows][channels] io_dtype;  dx, dz [rows][channels] y_dtype (dz: required
+ *  with z, NULL without);  dweight, dbias [channels] fp32, nullable, summed
+ *  over the rows in a fixed order (no atomics)
+ *  workspace  >= ssd_group_norm_bwd_workspace_size bytes, 256-byte aligned
+ * Errors: as ssd_group_norm_fwd, and SSD_ERR_WORKSPACE.
+ */
+ssd_status_t ssd_group_norm_bwd(const ssd_group_norm_desc_t* desc, const void* x, const void* z, const float* weight,
+                                const float* bias, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ssd_group_norm_bwd needs for `desc`.  Pure host function. */
+ssd_status_t ssd_group_norm_bwd_workspace_size(const ssd_group_norm_desc_t* desc, size_t* bytes);
 
 /*
  * Synchronises `stream`, then reports (and clears) the device-side error word

@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "../../include/ssd.h"
+#include "ssd_checks.h"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
 
@@ -33,21 +34,6 @@ static cudaError_t device_error_ptr(unsigned** out) {
     *out = g_err_ptr[dev];
     return cudaSuccess;
 }
-
-static inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
-static bool valid_dtype(int32_t d) { return d == SSD_F32 || d == SSD_BF16; }
-static size_t dsize(int32_t d) { return d == SSD_BF16 ? 2 : 4; }
-
-static bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
 static ssd_status_t check_prefill_desc(const ssd_prefill_desc_t* d) {
     if (!d) return SSD_ERR_INVALID_ARG;

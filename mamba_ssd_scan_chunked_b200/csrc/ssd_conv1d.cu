@@ -1,0 +1,345 @@
+// Short causal convolution along the tokens (2 to 4 taps per channel), its
+// single-token step and its backward pass.
+//
+//   v_t[c] = bias[c] + sum_{k < W} w[c][k] x_{t-W+1+k}[c];   y = v or silu(v)
+//   dv = dy silu'(v);  dx_s = sum_k w[k] dv_{s+W-1-k};  dw[k] = sum_t dv_t x_{t-W+1+k};  db = sum_t dv_t
+//
+// Every kernel is a stream bound by HBM: a thread owns a few neighbouring
+// channels, walks over a run of tokens with the last W - 1 inputs in registers,
+// and so reads each input once (and W - 1 more per run).
+#include "ssd_common.cuh"
+#include "ssd_internal.h"
+
+namespace ssd {
+
+// VEC consecutive elements (VEC * sizeof(T) is 8, 16 or 32 bytes) to and from fp32
+template <int VEC> __device__ __forceinline__ void loadv(const bf16* p, float* v) {
+    if constexpr (VEC == 8) {
+        load8(p, v);
+    } else {
+        const uint2 r = *reinterpret_cast<const uint2*>(p);
+        v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xffff0000u);
+        v[2] = __uint_as_float(r.y << 16); v[3] = __uint_as_float(r.y & 0xffff0000u);
+    }
+}
+template <int VEC> __device__ __forceinline__ void loadv(const float* p, float* v) {
+    if constexpr (VEC == 8) load8(p, v);
+    else Vec16<float>::load(p, v);
+}
+template <int VEC> __device__ __forceinline__ void storev(bf16* p, const float* v) {
+    if constexpr (VEC == 8) {
+        store8(p, v);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                  *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+template <int VEC> __device__ __forceinline__ void storev(float* p, const float* v) {
+    if constexpr (VEC == 8) store8(p, v);
+    else Vec16<float>::store(p, v);
+}
+template <int VEC> __device__ __forceinline__ void load_state(const void* p, bool is_bf16, int64_t i, float* v) {
+    if (is_bf16) loadv<VEC>((const bf16*)p + i, v);
+    else loadv<VEC>((const float*)p + i, v);
+}
+template <int VEC> __device__ __forceinline__ void store_state(void* p, bool is_bf16, int64_t i, const float* v) {
+    if (is_bf16) storev<VEC>((bf16*)p + i, v);
+    else storev<VEC>((float*)p + i, v);
+}
+
+// weight [D][W] of channels c .. c + VEC as w[k][i]
+template <int W, int VEC>
+__device__ __forceinline__ void load_taps(const float* w, int64_t c, float (&out)[W][VEC]) {
+    float raw[W * VEC];
+#pragma unroll
+    for (int i = 0; i < W * VEC / 4; ++i) Vec16<float>::load(w + c * W + 4 * i, raw + 4 * i);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int k = 0; k < W; ++k) out[k][i] = raw[i * W + k];
+}
+
+// where channel c lies in the split tensors: tensor index, its row length and c's place in the row
+__device__ __forceinline__ int split_of(const Conv1dArgs& a, int64_t c, int64_t* ld, int64_t* at) {
+    if (c < a.part[0]) { *ld = a.part[0]; *at = c; return 0; }
+    c -= a.part[0];
+    if (c < a.part[1]) { *ld = a.part[1]; *at = c; return 1; }
+    *ld = a.part[2]; *at = c - a.part[1];
+    return 2;
+}
+
+// the W - 1 inputs before token t0 of a sequence that starts at token p: kept
+// inputs where they lie before p (t0 < p: as of token p)
+template <typename IoT, int W, int VEC>
+__device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int64_t c, int64_t t0, int64_t p,
+                                            float (&win)[W][VEC]) {
+    const int64_t from = t0 < p ? p : t0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int64_t s = from - (W - 1) + j;
+        if (s >= p) {
+            loadv<VEC>((const IoT*)a.x + (b * a.L + s) * a.xs + c, win[j]);
+        } else if (a.init) {
+            load_state<VEC>(a.init, a.state_bf16, (b * (W - 1) + (W - 1) + (s - p)) * a.D + c, win[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+        }
+    }
+}
+
+constexpr int kFwdThreads = 128, kFwdTokens = 16;
+
+template <typename IoT, typename YT, int W>
+__global__ void __launch_bounds__(kFwdThreads)
+conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
+    constexpr int VEC = 16 / sizeof(IoT);
+    const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * kFwdThreads + threadIdx.x) * VEC;
+    const int64_t bs = blockIdx.x / (unsigned)cblocks;
+    const int64_t b = bs / nseg, seg = bs % nseg;
+    if (c >= a.D) return;
+    int64_t p = a.pad_left ? a.pad_left[b] : 0;
+    p = p < 0 ? 0 : p > a.L ? a.L : p;
+    const int64_t t0 = seg * kFwdTokens;
+    const int64_t t1 = t0 + kFwdTokens < a.L ? t0 + kFwdTokens : a.L;
+
+    float w[W][VEC], bias[VEC], win[W][VEC];
+    load_taps<W, VEC>(a.w, c, w);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+    load_window<IoT, W, VEC>(a, b, c, t0, p, win);
+    int64_t ld, at;
+    const int which = split_of(a, c, &ld, &at);
+    YT* y = (YT*)a.y[which] + (b * a.L) * ld + at;
+    for (int64_t t = t0; t < t1; ++t) {
+        float out[VEC];
+        if (t >= p) {
+            loadv<VEC>((const IoT*)a.x + (b * a.L + t) * a.xs + c, win[W - 1]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                float v = bias[i];
+#pragma unroll
+                for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[k][i], v);
+                out[i] = a.silu ? v * sigmoid_f32(v) : v;
+            }
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) win[k][i] = win[k + 1][i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) out[i] = 0.f;
+        }
+        storev<VEC>(y + t * ld, out);
+    }
+    if (a.final_state && seg == nseg - 1) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            store_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, win[j]);
+    }
+}
+
+// One token: a thread owns VEC channels of a sequence, so its state is read and
+// written by no other thread.
+template <typename IoT, typename YT, int W>
+__global__ void __launch_bounds__(kFwdThreads)
+conv1d_update_kernel(const Conv1dArgs a, int cblocks) {
+    constexpr int VEC = 16 / sizeof(IoT);
+    const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * kFwdThreads + threadIdx.x) * VEC;
+    const int64_t b = blockIdx.x / (unsigned)cblocks;
+    if (c >= a.D) return;
+    float w[W][VEC], win[W][VEC], out[VEC];
+    loadv<VEC>((const IoT*)a.x + b * a.xs + c, win[W - 1]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+        load_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, win[j]);
+    load_taps<W, VEC>(a.w, c, w);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        float v = a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[k][i], v);
+        out[i] = a.silu ? v * sigmoid_f32(v) : v;
+    }
+    int64_t ld, at;
+    const int which = split_of(a, c, &ld, &at);
+    storev<VEC>((YT*)a.y[which] + b * ld + at, out);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+        store_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, win[j + 1]);
+}
+
+// Backward.  A block is 32 lanes (4 channels each) x 8 warps; warp q walks over
+// the kBwdTokens tokens of its run and the W - 1 after it (whose dv its last dx
+// need).  dx of a token is complete W - 1 tokens later.  The block's sums of dw
+// and db go to one row of the partial sums.
+constexpr int kBwdWarps = 8, kBwdTokens = 16, kBwdVec = 4;
+
+template <typename IoT, typename GT, int W>
+__global__ void __launch_bounds__(kBwdWarps * 32)
+conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
+    constexpr int VEC = kBwdVec;
+    __shared__ float sums[kBwdWarps][(W + 1) * VEC][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * 32 + lane) * VEC;
+    const int64_t bs = blockIdx.x / (unsigned)cblocks;
+    const int64_t b = bs / nseg, seg = bs % nseg;
+    const int64_t t0 = (seg * kBwdWarps + warp) * kBwdTokens;
+    const int64_t t1 = t0 + kBwdTokens < a.L ? t0 + kBwdTokens : a.L;
+    float dw[W][VEC], db[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
+    }
+    if (c < a.D && (t0 < a.L || t0 == 0)) {
+        float w[W][VEC], bias[VEC], win[W][VEC], pend[W][VEC];
+        load_taps<W, VEC>(a.w, c, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+        load_window<IoT, W, VEC>(a, b, c, t0, 0, win);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) pend[k][i] = 0.f;
+        int64_t ld, at;
+        const int which = split_of(a, c, &ld, &at);
+        const IoT* dy = (const IoT*)a.dy[which] + (b * a.L) * ld + at;
+        for (int64_t t = t0; t < t1 + W - 1; ++t) {
+            if (t < a.L) {
+                float dv[VEC];
+                loadv<VEC>((const IoT*)a.x + (b * a.L + t) * a.xs + c, win[W - 1]);
+                loadv<VEC>(dy + t * ld, dv);
+                const bool mine = t < t1;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (a.silu) {
+                        float v = bias[i];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[k][i], v);
+                        const float g = sigmoid_f32(v);
+                        dv[i] *= g * fmaf(v, 1.f - g, 1.f);
+                    }
+                    if (mine) {
+                        db[i] += dv[i];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) dw[k][i] = fmaf(dv[i], win[k][i], dw[k][i]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < W; ++k) pend[k][i] = fmaf(w[k][i], dv[i], pend[k][i]);
+                }
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) win[k][i] = win[k + 1][i];
+            }
+            const int64_t s = t - (W - 1);            // the input whose gradient is now complete
+            if (s >= t0 || t0 == 0) {
+                if (a.dfinal && s >= a.L - (W - 1)) {
+                    float f[VEC];
+                    load_state<VEC>(a.dfinal, a.state_bf16, (b * (W - 1) + s - a.L + W - 1) * a.D + c, f);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) pend[0][i] += f[i];
+                }
+                if (s >= 0) storev<VEC>((GT*)a.dx + (b * a.L + s) * a.dxs + c, pend[0]);
+                else if (a.dinit)
+                    store_state<VEC>(a.dinit, a.state_bf16, (b * (W - 1) + s + W - 1) * a.D + c, pend[0]);
+            }
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) pend[k][i] = pend[k + 1][i];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) pend[W - 1][i] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) sums[warp][i * W + k][lane] = dw[k][i];
+        sums[warp][W * VEC + i][lane] = db[i];
+    }
+    __syncthreads();
+    float* row = a.ws + bs * (a.D * (W + 1));
+    for (int e = warp; e < (W + 1) * VEC; e += kBwdWarps) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kBwdWarps; ++q) s += sums[q][e][lane];
+        if (c < a.D) row[e < W * VEC ? c * W + e : a.D * W + c + (e - W * VEC)] = s;
+    }
+}
+
+// batch or seqlen 0: parameter gradients 0 (the batch 0 case)
+__global__ void conv1d_zero_kernel(float* dw, float* db, int64_t nw, int64_t nb) {
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < nw + nb; i += (int64_t)gridDim.x * blockDim.x) {
+        if (i < nw) dw[i] = 0.f;
+        else if (db) db[i - nw] = 0.f;
+    }
+}
+
+static int64_t fwd_segments(int64_t L) { return L > 0 ? (L + kFwdTokens - 1) / kFwdTokens : 1; }
+
+static int64_t bwd_segments(int64_t L) {
+    const int64_t run = kBwdWarps * kBwdTokens;
+    return L > 0 ? (L + run - 1) / run : 1;
+}
+
+int64_t conv1d_bwd_segments(int64_t batch, int64_t L) { return batch * bwd_segments(L); }
+
+int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D) {
+    return batch * fwd_segments(L) * ((D / 4 + 31) / 32);
+}
+
+// calls f<IoT, OutT, W>() for the types and taps of a
+#define CONV1D_DISPATCH(FN)                                                                    \
+    do {                                                                                       \
+        if (a.io_bf16) {                                                                       \
+            if (a.y_bf16) { if (a.W == 2) FN(bf16, bf16, 2); else if (a.W == 3) FN(bf16, bf16, 3); else FN(bf16, bf16, 4); } \
+            else { if (a.W == 2) FN(bf16, float, 2); else if (a.W == 3) FN(bf16, float, 3); else FN(bf16, float, 4); } \
+        } else {                                                                               \
+            if (a.y_bf16) { if (a.W == 2) FN(float, bf16, 2); else if (a.W == 3) FN(float, bf16, 3); else FN(float, bf16, 4); } \
+            else { if (a.W == 2) FN(float, float, 2); else if (a.W == 3) FN(float, float, 3); else FN(float, float, 4); } \
+        }                                                                                      \
+    } while (0)
+
+cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s) {
+    const int vec = a.io_bf16 ? 8 : 4;
+    const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads), nseg = (int)fwd_segments(a.L);
+    const unsigned grid = (unsigned)(a.batch * nseg * cblocks);
+#define FN(IO, Y, W_) conv1d_fwd_kernel<IO, Y, W_><<<grid, kFwdThreads, 0, s>>>(a, cblocks, nseg)
+    CONV1D_DISPATCH(FN);
+#undef FN
+    return cudaGetLastError();
+}
+
+cudaError_t launch_conv1d_update(const Conv1dArgs& a, cudaStream_t s) {
+    const int vec = a.io_bf16 ? 8 : 4;
+    const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads);
+    const unsigned grid = (unsigned)(a.batch * cblocks);
+#define FN(IO, Y, W_) conv1d_update_kernel<IO, Y, W_><<<grid, kFwdThreads, 0, s>>>(a, cblocks)
+    CONV1D_DISPATCH(FN);
+#undef FN
+    return cudaGetLastError();
+}
+
+cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s) {
+    const int64_t nw = a.D * a.W;
+    if (a.batch == 0) {
+        conv1d_zero_kernel<<<(unsigned)((nw + a.D + 255) / 256), 256, 0, s>>>(a.dw, a.db, nw, a.D);
+        return cudaGetLastError();
+    }
+    const int cblocks = (int)((a.D / kBwdVec + 31) / 32), nseg = (int)bwd_segments(a.L);
+    const unsigned grid = (unsigned)(a.batch * nseg * cblocks);
+#define FN(IO, G_, W_) conv1d_bwd_kernel<IO, G_, W_><<<grid, kBwdWarps * 32, 0, s>>>(a, cblocks, nseg)
+    CONV1D_DISPATCH(FN);
+#undef FN
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_column_sum(a.ws, a.batch * nseg, nw + a.D, nw, a.dw, false, s);
+    if (e != cudaSuccess || !a.db) return e;
+    return launch_column_sum(a.ws + nw, a.batch * nseg, nw + a.D, a.D, a.db, false, s);
+}
+
+}  // namespace ssd

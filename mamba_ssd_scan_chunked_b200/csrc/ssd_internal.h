@@ -206,6 +206,75 @@ struct Mamba3Args {
 cudaError_t launch_mamba3(const Mamba3Args& a, cudaStream_t s);
 int mamba3_launches(bool tc, bool io_bf16, bool has_lam, bool has_theta, bool has_final, bool fused);
 
+// Short causal convolution (ssd_conv1d.cu).  The channels go to (come from) up
+// to three dense tensors of part[0..2] channels.
+struct Conv1dArgs {
+    int64_t batch, L, D, W, xs, dxs, part[3];
+    bool io_bf16, y_bf16, state_bf16, silu;
+    const void* x;
+    const float *w, *bias;          // [D][W], [D]
+    const void *init, *dfinal;      // [b][W-1][D]
+    const int32_t* pad_left;
+    void* y[3];
+    void* final_state;              // the update's state
+    const void* dy[3];
+    void *dx, *dinit;
+    float *dw, *db;
+    float* ws;                      // backward: [segments][D W + D] partial sums
+};
+
+cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s);
+cudaError_t launch_conv1d_update(const Conv1dArgs& a, cudaStream_t s);
+cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s);
+// token segments of the backward (rows of its partial sums); 0 for an empty batch
+int64_t conv1d_bwd_segments(int64_t batch, int64_t L);
+// blocks the forward and backward launch at most (their grids are one-dimensional)
+int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D);
+
+// Selective scan (ssd_selective.cu, ssd_selective_bwd.cu).
+struct SelectiveArgs {
+    int64_t batch, L, D, N, G, zs;
+    bool io_bf16, y_bf16, state_bf16;
+    const void *x, *dt_raw, *B, *C, *z, *init;
+    const float *dt_bias, *A, *Dv;
+    const int32_t* pad_left;
+    void *y, *final_state;          // the update's state is final_state
+    const void *dy, *dfinal;
+    void *dx, *ddt, *dB, *dC, *dz, *dinit;
+    float *dA, *ddt_bias, *dD;
+    char* ws;
+};
+
+size_t selective_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
+size_t selective_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
+// an upper bound of any of its kernels' blocks
+int64_t selective_blocks(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
+cudaError_t launch_selective_fwd(const SelectiveArgs& a, cudaStream_t s);
+cudaError_t launch_selective_update(const SelectiveArgs& a, cudaStream_t s);
+cudaError_t launch_selective_bwd(const SelectiveArgs& a, cudaStream_t s);
+
+// Group normalisation (ssd_group_norm.cu).
+struct GroupNormArgs {
+    int64_t rows, C, G, zs;
+    bool x_bf16, io_bf16, y_bf16, center;
+    int act;                        // ssd_norm_activation_t
+    float eps;
+    const void *x, *z, *dy;
+    const float *w, *bias;
+    void *y, *dx, *dz;
+    float *dw, *db;
+    float* ws;                      // backward: partial sums of dw, then of db
+};
+
+size_t group_norm_bwd_workspace(int64_t rows, int64_t C, int64_t G);
+cudaError_t launch_group_norm_fwd(const GroupNormArgs& a, cudaStream_t s);
+cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s);
+
+// out[c] = sum of column c of part [rows][stride], c < cols, in a fixed order
+// (ssd_column_sum.cu); out is bf16 or fp32
+cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t stride, int64_t cols, void* out, bool out_bf16,
+                              cudaStream_t s);
+
 // fault-injection bits set by ssd_debug_inject (read at every launch)
 uint32_t debug_faults();
 

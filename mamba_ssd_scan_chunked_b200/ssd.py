@@ -7,7 +7,12 @@ first call raises.
 
 Raw names mirror the C ABI (``ssd_chunk_scan_fwd``, ``ssd_state_update``, ...)
 and take integer device pointers; ``chunk_scan_fwd`` and ``state_update`` are
-the tensor-level conveniences (shape checks, output and workspace allocation).
+the tensor-level conveniences (shape checks, output and workspace allocation),
+as are those of the operators around the scan (``conv1d_fwd``, ``conv1d_update``,
+``conv1d_bwd``, ``selective_scan_fwd``, ``selective_state_update``,
+``selective_scan_bwd``, ``group_norm_fwd``, ``group_norm_bwd``).  These work on
+the device of their tensors and, unless ``stream`` is given, on its current
+stream; outputs and workspaces that they allocate belong to the launching stream.
 """
 from __future__ import annotations
 
@@ -31,7 +36,11 @@ EXPORTS = ("ssd_version", "ssd_status_string", "ssd_chunk_scan_workspace_size", 
            "ssd_chunk_scan_fwd_mamba3", "ssd_chunk_scan_mamba3_workspace_size", "ssd_chunk_scan_mamba3_launches",
            "ssd_state_update", "ssd_state_update_mimo", "ssd_state_update_mamba3",
            "ssd_replay_buffer_size",
-           "ssd_replay_step", "ssd_get_device_error", "ssd_debug_inject")
+           "ssd_replay_step", "ssd_get_device_error", "ssd_debug_inject",
+           "ssd_conv1d_fwd", "ssd_conv1d_update", "ssd_conv1d_bwd", "ssd_conv1d_bwd_workspace_size",
+           "ssd_selective_scan_fwd", "ssd_selective_scan_workspace_size", "ssd_selective_state_update",
+           "ssd_selective_scan_bwd", "ssd_selective_scan_bwd_workspace_size",
+           "ssd_group_norm_fwd", "ssd_group_norm_bwd", "ssd_group_norm_bwd_workspace_size")
 
 # fault-injection bits of ssd_debug_inject
 SSD_FAULT_DROP_RUN_PUBLISH = 0x1
@@ -70,6 +79,29 @@ class ReplayDesc(ctypes.Structure):
                 ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
                 ("y_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("capacity", ctypes.c_int32)]
 
+
+class Conv1dDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+                ("split1", ctypes.c_int64), ("split2", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class SelectiveDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32)]
+
+
+class GroupNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("center", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
+# ssd_norm_activation_t
+SSD_NORM_NONE, SSD_NORM_SILU, SSD_NORM_GATE_AFTER, SSD_NORM_GATE_BEFORE = 0, 1, 2, 3
 
 _lock = threading.Lock()
 _lib = None
@@ -129,6 +161,21 @@ def lib():
             L.ssd_get_device_error.argtypes = [_VP, ctypes.POINTER(ctypes.c_uint32)]
             L.ssd_debug_inject.restype = ctypes.c_int
             L.ssd_debug_inject.argtypes = [ctypes.c_uint32]
+            size = [ctypes.POINTER(ctypes.c_size_t)]
+            for name, desc, args in (
+                    ("ssd_conv1d_fwd", Conv1dDesc, [_VP] * 10), ("ssd_conv1d_update", Conv1dDesc, [_VP] * 8),
+                    ("ssd_conv1d_bwd", Conv1dDesc, [_VP] * 13 + [ctypes.c_size_t, _VP]),
+                    ("ssd_conv1d_bwd_workspace_size", Conv1dDesc, size),
+                    ("ssd_selective_scan_fwd", SelectiveDesc, [_VP] * 13 + [ctypes.c_size_t, _VP]),
+                    ("ssd_selective_scan_workspace_size", SelectiveDesc, size),
+                    ("ssd_selective_state_update", SelectiveDesc, [_VP] * 11),
+                    ("ssd_selective_scan_bwd", SelectiveDesc, [_VP] * 21 + [ctypes.c_size_t, _VP]),
+                    ("ssd_selective_scan_bwd_workspace_size", SelectiveDesc, size),
+                    ("ssd_group_norm_fwd", GroupNormDesc, [_VP] * 6),
+                    ("ssd_group_norm_bwd", GroupNormDesc, [_VP] * 10 + [ctypes.c_size_t, _VP]),
+                    ("ssd_group_norm_bwd_workspace_size", GroupNormDesc, size)):
+                getattr(L, name).restype = ctypes.c_int
+                getattr(L, name).argtypes = [ctypes.POINTER(desc)] + args
             _lib = L
     return _lib
 
@@ -279,6 +326,83 @@ def ssd_get_device_error(stream=None):
 def ssd_debug_inject(faults: int) -> int:
     """Test hook: fault bits injected into every following launch (0 clears)."""
     return lib().ssd_debug_inject(int(faults))
+
+
+def ssd_conv1d_fwd(desc, x, weight, bias, init_state, pad_left, y0, y1, y2, final_state, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    ptrs = (x, weight, bias, init_state, pad_left, y0, y1, y2, final_state, stream)
+    return lib().ssd_conv1d_fwd(ctypes.byref(desc), *(p or None for p in ptrs))
+
+
+def ssd_conv1d_update(desc, state, x, weight, bias, y0, y1, y2, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    return lib().ssd_conv1d_update(ctypes.byref(desc), *(p or None for p in (state, x, weight, bias, y0, y1, y2, stream)))
+
+
+def ssd_conv1d_bwd(desc, x, weight, bias, init_state, dy0, dy1, dy2, dfinal_state, dx, dweight, dbias, dinit_state,
+                   workspace, workspace_bytes, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    ptrs = (x, weight, bias, init_state, dy0, dy1, dy2, dfinal_state, dx, dweight, dbias, dinit_state, workspace)
+    return lib().ssd_conv1d_bwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes), stream or None)
+
+
+def ssd_selective_scan_fwd(desc, x, dt_raw, dt_bias, A, B, C, D, z, init_state, pad_left, y, final_state, workspace,
+                           workspace_bytes, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    ptrs = (x, dt_raw, dt_bias, A, B, C, D, z, init_state, pad_left, y, final_state, workspace)
+    return lib().ssd_selective_scan_fwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes),
+                                        stream or None)
+
+
+def ssd_selective_state_update(desc, state, x, dt_raw, dt_bias, A, B, C, D, z, y, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    ptrs = (state, x, dt_raw, dt_bias, A, B, C, D, z, y, stream)
+    return lib().ssd_selective_state_update(ctypes.byref(desc), *(p or None for p in ptrs))
+
+
+def ssd_selective_scan_bwd(desc, x, dt_raw, dt_bias, A, B, C, D, z, init_state, dy, dfinal_state, dx, ddt_raw,
+                           ddt_bias, dA, dB, dC, dD, dz, dinit_state, workspace, workspace_bytes, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    ptrs = (x, dt_raw, dt_bias, A, B, C, D, z, init_state, dy, dfinal_state, dx, ddt_raw, ddt_bias, dA, dB, dC, dD,
+            dz, dinit_state, workspace)
+    return lib().ssd_selective_scan_bwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes),
+                                        stream or None)
+
+
+def ssd_group_norm_fwd(desc, x, z, weight, bias, y, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    return lib().ssd_group_norm_fwd(ctypes.byref(desc), *(p or None for p in (x, z, weight, bias, y, stream)))
+
+
+def ssd_group_norm_bwd(desc, x, z, weight, bias, dy, dx, dz, dweight, dbias, workspace, workspace_bytes, stream) -> int:
+    """Raw call; returns the status code (0 = enqueued)."""
+    ptrs = (x, z, weight, bias, dy, dx, dz, dweight, dbias, workspace)
+    return lib().ssd_group_norm_bwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes),
+                                    stream or None)
+
+
+def _size_of(name, desc) -> int:
+    n = ctypes.c_size_t(0)
+    st = getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(n))
+    if st:
+        raise SsdError(st, name)
+    return n.value
+
+
+def ssd_conv1d_bwd_workspace_size(desc: Conv1dDesc) -> int:
+    return _size_of("ssd_conv1d_bwd_workspace_size", desc)
+
+
+def ssd_selective_scan_workspace_size(desc: SelectiveDesc) -> int:
+    return _size_of("ssd_selective_scan_workspace_size", desc)
+
+
+def ssd_selective_scan_bwd_workspace_size(desc: SelectiveDesc) -> int:
+    return _size_of("ssd_selective_scan_bwd_workspace_size", desc)
+
+
+def ssd_group_norm_bwd_workspace_size(desc: GroupNormDesc) -> int:
+    return _size_of("ssd_group_norm_bwd_workspace_size", desc)
 
 
 # --------------------------------------------------------------------------
@@ -598,3 +722,431 @@ def state_update_mimo(state, x, dt_raw, dt_bias, A, B, C, D, *, y=None, y_dtype=
     if st:
         raise SsdError(st, "ssd_state_update_mimo")
     return y
+
+
+# --------------------------------------------------------------------------
+# the operators around the scan
+# --------------------------------------------------------------------------
+def _row_stride(t, name, lead, width, dtype):
+    """Elements from a row of ``t`` (shape ``lead + (width,)``, possibly columns cut out of wider
+    rows) to the next one; the rows follow each other at one distance."""
+    _expect(t, tuple(lead) + (width,), name, dtype)
+    if t.numel() == 0:
+        return width
+    if t.stride(-1) != 1 and width > 1:
+        raise ValueError(f"{name}: the channels have to be neighbours in memory")
+    stride, rows = None, 1
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1:
+            if stride is None:
+                stride = st
+            elif st != stride * rows:
+                raise ValueError(f"{name}: rows at one distance expected, strides {t.stride()}")
+        rows *= n
+    if stride is None:
+        return width
+    if stride < width:
+        raise ValueError(f"{name}: overlapping rows, strides {t.stride()}")
+    return stride
+
+
+def _on_one_device(dense, rows=()):
+    """The CUDA device of all the tensors (None passes); the ``dense`` ones have to be contiguous."""
+    device = None
+    for t in (*dense, *rows):
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libssd takes contiguous CUDA tensors")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: libssd takes them on one device")
+    for t in dense:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("libssd takes contiguous CUDA tensors")
+    return device
+
+
+class _LaunchOn:
+    """Makes ``device`` the current one and ``stream`` (None: the device's current stream) the stream
+    that outputs and workspaces are allocated for; gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.contexts = []
+        if device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        self.contexts.append(torch.cuda.stream(stream))
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return int(self.handle)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace when it is large enough, else one of this call's own."""
+    import torch
+    if workspace is not None and workspace.numel() * workspace.element_size() >= need:
+        return workspace, workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def _check_workspace(workspace):
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous CUDA tensor")
+
+
+def _check_pad(pad_left, batch):
+    import torch
+    if pad_left is not None:
+        _expect(pad_left, (batch,), "pad_left", torch.int32)
+
+
+def _silu_flag(activation) -> int:
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation: {activation!r}, expected None or 'silu'")
+    return 0 if activation is None else 1
+
+
+def _split_widths(split, channels):
+    widths = (channels,) if split is None else tuple(int(n) for n in split)
+    if not 1 <= len(widths) <= 3 or min(widths) < 1 or sum(widths) != channels:
+        raise ValueError(f"split: {split}, expected one to three widths that add up to {channels} channels")
+    return widths
+
+
+def _conv_outputs(y, widths, lead, dtype, one):
+    """The given outputs, checked, or None for each."""
+    if y is None:
+        return [None] * len(widths)
+    y = [y] if one and hasattr(y, "shape") else list(y)
+    if len(y) != len(widths):
+        raise ValueError(f"y: {len(y)} tensors, expected {len(widths)}")
+    for t, n in zip(y, widths):
+        _expect(t, tuple(lead) + (n,), "y", dtype)
+    return y
+
+
+def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation="silu", pad_left=None, y=None,
+               final_state=None, y_dtype=None, state_dtype=None, want_final_state=True, stream=None):
+    """Short causal convolution: x [b,L,D] (columns of wider rows are taken), weight [D,W] and bias [D] fp32,
+    W = 2, 3 or 4; the W - 1 inputs before the first token are init_state [b,W-1,D]'s.
+
+    ``split``: widths of up to three dense output tensors (as the scan takes x, B and C); None gives one.
+    ``pad_left`` (int32 [b], CUDA): leading tokens that are absent; y is 0 there.
+    Returns (y, final_state): a tensor, with ``split`` a tuple of them, and the kept inputs [b,W-1,D]
+    (None without ``want_final_state``); state_dtype defaults to init_state's dtype, else fp32.
+    """
+    import torch
+    b, L, D = x.shape
+    W = weight.shape[1]
+    widths = _split_widths(split, D)
+    xs = _row_stride(x, "x", (b, L), D, None)
+    if y_dtype is None:
+        y_dtype = x.dtype if y is None else (y if hasattr(y, "dtype") else y[0]).dtype
+    if state_dtype is None:
+        state_dtype = (init_state.dtype if init_state is not None else
+                       final_state.dtype if final_state is not None else torch.float32)
+    _expect(weight, (D, W), "weight", torch.float32)
+    _expect(bias, (D,), "bias", torch.float32)
+    _expect(init_state, (b, W - 1, D), "init_state", state_dtype)
+    _expect(final_state, (b, W - 1, D), "final_state", state_dtype)
+    _check_pad(pad_left, b)
+    out = _conv_outputs(y, widths, (b, L), y_dtype, split is None)
+    desc = Conv1dDesc(b, L, D, W, xs, D, *(widths[1:] + (0, 0))[:2], _dtype_code(x.dtype), _dtype_code(y_dtype),
+                      _dtype_code(state_dtype), _silu_flag(activation))
+    device = _on_one_device((weight, bias, init_state, pad_left, final_state, *out), (x,))
+    with _LaunchOn(device, stream) as handle:
+        out = [torch.empty((b, L, n), dtype=y_dtype, device=device) if t is None else t for t, n in zip(out, widths)]
+        if final_state is None and want_final_state:
+            final_state = torch.empty((b, W - 1, D), dtype=state_dtype, device=device)
+        st = ssd_conv1d_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(init_state), _ptr(pad_left),
+                            *([_ptr(t) for t in out] + [0, 0])[:3], _ptr(final_state), handle)
+    if st:
+        raise SsdError(st, "ssd_conv1d_fwd")
+    return (out[0] if split is None else tuple(out)), final_state
+
+
+def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu", y=None, y_dtype=None, stream=None):
+    """One token of ``conv1d_fwd``, in place on the kept inputs ``state`` [b,W-1,D]: x [b,D] (columns of wider
+    rows are taken).  Returns y [b,D], with ``split`` a tuple of tensors."""
+    import torch
+    b, D = x.shape
+    W = weight.shape[1]
+    widths = _split_widths(split, D)
+    xs = _row_stride(x, "x", (b,), D, None)
+    if y_dtype is None:
+        y_dtype = x.dtype if y is None else (y if hasattr(y, "dtype") else y[0]).dtype
+    _expect(weight, (D, W), "weight", torch.float32)
+    _expect(bias, (D,), "bias", torch.float32)
+    _expect(state, (b, W - 1, D), "state")
+    out = _conv_outputs(y, widths, (b,), y_dtype, split is None)
+    desc = Conv1dDesc(b, 1, D, W, xs, D, *(widths[1:] + (0, 0))[:2], _dtype_code(x.dtype), _dtype_code(y_dtype),
+                      _dtype_code(state.dtype), _silu_flag(activation))
+    device = _on_one_device((state, weight, bias, *out), (x,))
+    with _LaunchOn(device, stream) as handle:
+        out = [torch.empty((b, n), dtype=y_dtype, device=device) if t is None else t for t, n in zip(out, widths)]
+        st = ssd_conv1d_update(desc, _ptr(state), _ptr(x), _ptr(weight), _ptr(bias),
+                               *([_ptr(t) for t in out] + [0, 0])[:3], handle)
+    if st:
+        raise SsdError(st, "ssd_conv1d_update")
+    return out[0] if split is None else tuple(out)
+
+
+def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activation="silu", dx=None,
+               grad_dtype=None, state_dtype=None, want_dinit=True, workspace=None, stream=None):
+    """Backward pass of ``conv1d_fwd`` (without padding): gradients of sum<dy, y> + <dfinal_state, final_state>.
+
+    ``dy``: a tensor [b,L,D] or the tuple of the split outputs' gradients, in x's dtype.  ``dx`` may be given,
+    as columns of wider rows too (the other columns are left as they were); else it is allocated dense, in
+    ``grad_dtype`` (default x's dtype).  Returns a dict: dx, dweight [D,W] and dbias [D] fp32 (None without
+    bias), dinit_state [b,W-1,D] (None without ``want_dinit``).
+    """
+    import torch
+    b, L, D = x.shape
+    W = weight.shape[1]
+    dys = [dy] if hasattr(dy, "shape") else list(dy)
+    widths = _split_widths([t.shape[-1] for t in dys], D)
+    xs = _row_stride(x, "x", (b, L), D, None)
+    if grad_dtype is None:
+        grad_dtype = dx.dtype if dx is not None else x.dtype
+    dxs = D if dx is None else _row_stride(dx, "dx", (b, L), D, grad_dtype)
+    if state_dtype is None:
+        src = init_state if init_state is not None else dfinal_state
+        state_dtype = src.dtype if src is not None else torch.float32
+    _expect(weight, (D, W), "weight", torch.float32)
+    _expect(bias, (D,), "bias", torch.float32)
+    _expect(init_state, (b, W - 1, D), "init_state", state_dtype)
+    _expect(dfinal_state, (b, W - 1, D), "dfinal_state", state_dtype)
+    for t, n in zip(dys, widths):
+        _expect(t, (b, L, n), "dy", x.dtype)
+    desc = Conv1dDesc(b, L, D, W, xs, dxs, *(widths[1:] + (0, 0))[:2], _dtype_code(x.dtype), _dtype_code(grad_dtype),
+                      _dtype_code(state_dtype), _silu_flag(activation))
+    _check_workspace(workspace)
+    device = _on_one_device((weight, bias, init_state, dfinal_state, workspace, *dys), (x, dx))
+    need = ssd_conv1d_bwd_workspace_size(desc)
+    with _LaunchOn(device, stream) as handle:
+        f32 = {"dtype": torch.float32, "device": device}
+        out = {"dx": torch.empty((b, L, D), dtype=grad_dtype, device=device) if dx is None else dx,
+               "dweight": torch.empty((D, W), **f32), "dbias": torch.empty(D, **f32) if bias is not None else None,
+               "dinit_state": torch.empty((b, W - 1, D), dtype=state_dtype, device=device) if want_dinit else None}
+        workspace, nbytes = _workspace(workspace, need, device)
+        st = ssd_conv1d_bwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(init_state),
+                            *([_ptr(t) for t in dys] + [0, 0])[:3], _ptr(dfinal_state), _ptr(out["dx"]),
+                            _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dinit_state"]), _ptr(workspace), nbytes,
+                            handle)
+    if st:
+        raise SsdError(st, "ssd_conv1d_bwd")
+    return out
+
+
+def _selective_desc(x, B, z, lead, y_dtype, state_dtype) -> SelectiveDesc:
+    D, G, N = x.shape[-1], B.shape[-2], B.shape[-1]
+    b, L = (lead[0], 1) if len(lead) == 1 else lead
+    zs = D if z is None else _row_stride(z, "z", lead, D, x.dtype)
+    return SelectiveDesc(b, L, D, N, G, zs, _dtype_code(x.dtype), _dtype_code(y_dtype), _dtype_code(state_dtype))
+
+
+def _check_selective_args(lead, x, dt_raw, dt_bias, A, B, C, D):
+    import torch
+    ch, bc = x.shape[-1], tuple(B.shape[-2:])
+    _expect(x, tuple(lead) + (ch,), "x")
+    _expect(dt_raw, tuple(x.shape), "dt_raw", x.dtype)
+    _expect(B, tuple(lead) + bc, "B", x.dtype)
+    _expect(C, tuple(lead) + bc, "C", x.dtype)
+    _expect(A, (ch, bc[1]), "A", torch.float32)
+    _expect(dt_bias, (ch,), "dt_bias", torch.float32)
+    _expect(D, (ch,), "D", torch.float32)
+
+
+def selective_scan_fwd(x, dt_raw, dt_bias, A, B, C, D, z=None, init_state=None, *, y=None, final_state=None,
+                       y_dtype=None, state_dtype=None, want_final_state=True, pad_left=None, workspace=None,
+                       stream=None):
+    """Selective scan (a decay per channel and state): x, dt_raw [b,L,D], dt_bias and D [D] fp32 (may be None),
+    A [D,N] fp32, B, C [b,L,G,N], gate z [b,L,D] (columns of wider rows are taken; may be None), states [b,D,N].
+    ``pad_left`` (int32 [b], CUDA): leading tokens that are absent; y is 0 there.
+
+    Returns (y, final_state) (None without ``want_final_state``); state_dtype defaults to init_state's dtype,
+    else fp32.
+    """
+    import torch
+    b, L, ch = x.shape
+    N = B.shape[-1]
+    if y_dtype is None:
+        y_dtype = x.dtype if y is None else y.dtype
+    if state_dtype is None:
+        state_dtype = (init_state.dtype if init_state is not None else
+                       final_state.dtype if final_state is not None else torch.float32)
+    _check_selective_args((b, L), x, dt_raw, dt_bias, A, B, C, D)
+    _expect(init_state, (b, ch, N), "init_state", state_dtype)
+    _expect(final_state, (b, ch, N), "final_state", state_dtype)
+    _expect(y, (b, L, ch), "y", y_dtype)
+    _check_pad(pad_left, b)
+    desc = _selective_desc(x, B, z, (b, L), y_dtype, state_dtype)
+    _check_workspace(workspace)
+    device = _on_one_device((x, dt_raw, dt_bias, A, B, C, D, init_state, pad_left, y, final_state, workspace), (z,))
+    need = ssd_selective_scan_workspace_size(desc)
+    with _LaunchOn(device, stream) as handle:
+        if y is None:
+            y = torch.empty((b, L, ch), dtype=y_dtype, device=device)
+        if final_state is None and want_final_state:
+            final_state = torch.empty((b, ch, N), dtype=state_dtype, device=device)
+        workspace, nbytes = _workspace(workspace, need, device)
+        st = ssd_selective_scan_fwd(desc, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                                    _ptr(z), _ptr(init_state), _ptr(pad_left), _ptr(y), _ptr(final_state),
+                                    _ptr(workspace), nbytes, handle)
+    if st:
+        raise SsdError(st, "ssd_selective_scan_fwd")
+    return y, final_state
+
+
+def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=None, y_dtype=None, stream=None):
+    """One token of ``selective_scan_fwd``, in place on ``state`` [b,D,N]: x, dt_raw [b,D], B, C [b,G,N],
+    z [b,D] (columns of wider rows are taken).  Returns y [b,D]."""
+    import torch
+    b, ch = x.shape
+    if y_dtype is None:
+        y_dtype = x.dtype if y is None else y.dtype
+    _check_selective_args((b,), x, dt_raw, dt_bias, A, B, C, D)
+    _expect(state, (b, ch, B.shape[-1]), "state")
+    _expect(y, (b, ch), "y", y_dtype)
+    desc = _selective_desc(x, B, z, (b,), y_dtype, state.dtype)
+    device = _on_one_device((state, x, dt_raw, dt_bias, A, B, C, D, y), (z,))
+    with _LaunchOn(device, stream) as handle:
+        if y is None:
+            y = torch.empty((b, ch), dtype=y_dtype, device=device)
+        st = ssd_selective_state_update(desc, _ptr(state), _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(A), _ptr(B),
+                                        _ptr(C), _ptr(D), _ptr(z), _ptr(y), handle)
+    if st:
+        raise SsdError(st, "ssd_selective_state_update")
+    return y
+
+
+def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=None, dfinal_state=None, *,
+                       grad_dtype=None, state_dtype=None, want_dinit=True, workspace=None, stream=None):
+    """Backward pass of ``selective_scan_fwd`` (without padding): gradients of sum<dy, y> + <dfinal_state,
+    final_state>; dy [b,L,D] in x's dtype.
+
+    Returns a dict: dx, ddt_raw, dz [b,L,D], dB, dC [b,L,G,N] (``grad_dtype``, default x's dtype), dA [D,N],
+    ddt_bias, dD [D] (fp32), dinit_state [b,D,N] (None without ``want_dinit``); dz, ddt_bias and dD are None
+    where z, dt_bias and D are.
+    """
+    import torch
+    b, L, ch = x.shape
+    G, N = B.shape[-2:]
+    if grad_dtype is None:
+        grad_dtype = x.dtype
+    if state_dtype is None:
+        src = init_state if init_state is not None else dfinal_state
+        state_dtype = src.dtype if src is not None else torch.float32
+    _check_selective_args((b, L), x, dt_raw, dt_bias, A, B, C, D)
+    _expect(dy, (b, L, ch), "dy", x.dtype)
+    _expect(init_state, (b, ch, N), "init_state", state_dtype)
+    _expect(dfinal_state, (b, ch, N), "dfinal_state", state_dtype)
+    desc = _selective_desc(x, B, z, (b, L), grad_dtype, state_dtype)
+    _check_workspace(workspace)
+    device = _on_one_device((x, dt_raw, dt_bias, A, B, C, D, dy, init_state, dfinal_state, workspace), (z,))
+    need = ssd_selective_scan_bwd_workspace_size(desc)
+    with _LaunchOn(device, stream) as handle:
+        gd, f32 = {"dtype": grad_dtype, "device": device}, {"dtype": torch.float32, "device": device}
+        out = {"dx": torch.empty((b, L, ch), **gd), "ddt_raw": torch.empty((b, L, ch), **gd),
+               "dz": torch.empty((b, L, ch), **gd) if z is not None else None,
+               "dB": torch.empty((b, L, G, N), **gd), "dC": torch.empty((b, L, G, N), **gd),
+               "dA": torch.empty((ch, N), **f32), "ddt_bias": torch.empty(ch, **f32) if dt_bias is not None else None,
+               "dD": torch.empty(ch, **f32) if D is not None else None,
+               "dinit_state": torch.empty((b, ch, N), dtype=state_dtype, device=device) if want_dinit else None}
+        workspace, nbytes = _workspace(workspace, need, device)
+        st = ssd_selective_scan_bwd(desc, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                                    _ptr(z), _ptr(init_state), _ptr(dy), _ptr(dfinal_state), _ptr(out["dx"]),
+                                    _ptr(out["ddt_raw"]), _ptr(out["ddt_bias"]), _ptr(out["dA"]), _ptr(out["dB"]),
+                                    _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["dinit_state"]),
+                                    _ptr(workspace), nbytes, handle)
+    if st:
+        raise SsdError(st, "ssd_selective_scan_bwd")
+    return out
+
+
+def _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype) -> GroupNormDesc:
+    import torch
+    C, lead = x.shape[-1], tuple(x.shape[:-1])
+    rows = 1
+    for n in lead:
+        rows *= n
+    _expect(weight, (C,), "weight", torch.float32)
+    _expect(bias, (C,), "bias", torch.float32)
+    act, zs = _silu_flag(activation), C
+    if z is not None:
+        if act:
+            raise ValueError("activation: the gate z has its own SiLU")
+        zs = _row_stride(z, "z", lead, C, io_dtype)
+        act = SSD_NORM_GATE_BEFORE if gate_first else SSD_NORM_GATE_AFTER
+    return GroupNormDesc(rows, C, int(ngroups), zs, float(eps), _dtype_code(x.dtype), _dtype_code(io_dtype),
+                         _dtype_code(y_dtype), int(bool(center)), act)
+
+
+def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center=False, gate_first=True,
+                   activation=None, y=None, y_dtype=None, stream=None):
+    """Group normalisation of x [..., C] over the C / ngroups channels of a group in each row (the root mean
+    square form; ``center`` subtracts the mean first), weight and bias [C] fp32 (may be None).
+
+    With a gate z [..., C] (columns of wider rows are taken) x silu(z) is normalised, without ``gate_first``
+    the result is multiplied by silu(z); without one ``activation`` may be "silu".  Returns y [..., C]
+    (``y_dtype``, default z's dtype, else x's).
+    """
+    import torch
+    if y_dtype is None:
+        y_dtype = y.dtype if y is not None else z.dtype if z is not None else x.dtype
+    desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation,
+                      z.dtype if z is not None else x.dtype, y_dtype)
+    _expect(y, tuple(x.shape), "y", y_dtype)
+    device = _on_one_device((x, weight, bias, y), (z,))
+    with _LaunchOn(device, stream) as handle:
+        if y is None:
+            y = torch.empty(x.shape, dtype=y_dtype, device=device)
+        st = ssd_group_norm_fwd(desc, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(y), handle)
+    if st:
+        raise SsdError(st, "ssd_group_norm_fwd")
+    return y
+
+
+def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=False, gate_first=True,
+                   activation=None, grad_dtype=None, workspace=None, stream=None):
+    """Backward pass of ``group_norm_fwd``; dy [..., C] (and z) in one dtype.  Returns a dict: dx, dz [..., C]
+    (``grad_dtype``, default dy's dtype), dweight, dbias [C] fp32; None where z, weight, bias are."""
+    import torch
+    if grad_dtype is None:
+        grad_dtype = dy.dtype
+    desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, dy.dtype, grad_dtype)
+    _expect(dy, tuple(x.shape), "dy")
+    _check_workspace(workspace)
+    device = _on_one_device((x, weight, bias, dy, workspace), (z,))
+    need = ssd_group_norm_bwd_workspace_size(desc)
+    with _LaunchOn(device, stream) as handle:
+        f32 = {"dtype": torch.float32, "device": device}
+        out = {"dx": torch.empty(x.shape, dtype=grad_dtype, device=device),
+               "dz": torch.empty(x.shape, dtype=grad_dtype, device=device) if z is not None else None,
+               "dweight": torch.empty(x.shape[-1], **f32) if weight is not None else None,
+               "dbias": torch.empty(x.shape[-1], **f32) if bias is not None else None}
+        workspace, nbytes = _workspace(workspace, need, device)
+        st = ssd_group_norm_bwd(desc, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(out["dx"]),
+                                _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), nbytes,
+                                handle)
+    if st:
+        raise SsdError(st, "ssd_group_norm_bwd")
+    return out

@@ -1,0 +1,181 @@
+"""GPU parity of the selective scan, its token step and its backward pass with
+the float64 oracle, element by element."""
+import numpy as np
+import pytest
+
+from mamba_ssd_scan_chunked_b200 import inputs as I
+from mamba_ssd_scan_chunked_b200 import ssd
+from oracle import layer as O
+from tests.gpu_util import to_dev, torch
+from tests.layer_util import check, check_dict, dev, draw, f64, rows_of, t_dtype
+
+pytestmark = pytest.mark.gpu
+F, B = I.F32, I.BF16
+
+
+def case(b, L, D, N, G, io, state, init, gate, skip, seed):
+    rng = np.random.default_rng([seed, 9])
+    lead = (b, L) if L is not None else (b,)
+    return {"x": draw([seed, 0], lead + (D,), io), "dt_raw": draw([seed, 1], lead + (D,), io),
+            "dt_bias": I.to_storage(np.log(np.expm1(rng.uniform(1e-3, 1e-1, D))), F) if skip else None,
+            "A": I.to_storage(-np.arange(1, N + 1) * rng.uniform(0.8, 1.2, (D, N)), F),
+            "B": draw([seed, 2], lead + (G, N), io), "C": draw([seed, 3], lead + (G, N), io),
+            "D": draw([seed, 4], (D,), F) if skip else None,
+            "z": draw([seed, 5], lead + (D,), io) if gate else None,
+            "init": draw([seed, 6], (b, D, N), state, 0.5) if init else None}
+
+
+def on_gpu(c, extra=0):
+    d = {k: dev(v) for k, v in c.items()}
+    if c["z"] is not None:
+        d["z"] = rows_of(c["z"], extra)
+    return d
+
+
+def args(d):
+    return [d[k] for k in ("x", "dt_raw", "dt_bias", "A", "B", "C", "D")]
+
+
+@pytest.mark.parametrize("b,L,D,N,G,io,y,state,init,gate,skip,pad,extra", [
+    (2, 37, 24, 16, 1, F, F, F, True, True, True, None, 0),
+    (2, 70, 72, 16, 1, B, B, F, False, True, True, None, 24),
+    (1, 300, 136, 8, 1, F, F, F, True, False, True, None, 0),
+    (2, 33, 48, 24, 2, B, F, B, True, True, True, None, 8),              # padded states, two groups
+    (1, 65, 16, 64, 2, F, F, F, True, True, True, None, 0),
+    (2, 40, 24, 128, 1, B, B, F, True, False, False, None, 0),           # a warp of states a channel
+    (1, 20, 16, 136, 1, F, F, F, True, True, True, None, 0),             # more states than one round of lanes
+    (1, 19, 8, 256, 1, F, F, F, False, True, True, None, 0),
+    (1, 1500, 8, 16, 1, F, F, F, True, True, True, None, 0),             # long: few channels, many tokens
+    (1, 2100, 40, 40, 1, B, F, F, True, True, True, None, 0),
+    (4, 50, 40, 16, 1, F, F, F, True, True, True, [0, 1, 49, 50], 0),
+    (3, 700, 24, 16, 1, F, B, F, False, True, True, [699, 64, -1], 8),
+    (2, 1, 16, 16, 1, B, B, B, True, True, True, None, 0),
+    (2, 0, 16, 16, 1, F, F, F, True, True, True, None, 0),
+    (0, 4, 16, 16, 1, F, F, F, False, False, True, None, 0),
+])
+def test_selective_scan_fwd(b, L, D, N, G, io, y, state, init, gate, skip, pad, extra):
+    t = torch()
+    c = case(b, L, D, N, G, io, state, init, gate, skip, 400 + L + N)
+    d = on_gpu(c, extra)
+    if pad is not None:
+        for i, p in enumerate(pad):
+            for k in ("x", "dt_raw", "B", "C", "z"):
+                if d[k] is not None:
+                    d[k][i, :max(p, 0)] = float("nan") if i % 2 else float("inf")
+    got, final = ssd.selective_scan_fwd(*args(d), d["z"], d["init"], y_dtype=t_dtype(y), state_dtype=t_dtype(state),
+                                        pad_left=None if pad is None else t.tensor(pad, dtype=t.int32, device="cuda"))
+    f = {k: f64(v) for k, v in c.items()}
+    ref, fref = O.selective_scan(*args(f), f["z"], f["init"], pad)
+    check("y", got, ref)
+    check("final", final, fref)
+
+
+def test_strong_and_vanishing_decays():
+    """dt up to 30 (decays that underflow), dt that vanishes, A = 0 and positive A of a few states."""
+    c = case(2, 90, 24, 16, 1, F, F, True, False, True, 5)
+    rng = np.random.default_rng(6)
+    c["dt_raw"][rng.random(c["dt_raw"].shape) < 0.2] = 30.0
+    c["dt_raw"][rng.random(c["dt_raw"].shape) < 0.2] = -1e4
+    c["A"][:, 3] = 0.0
+    c["A"][::2, 5] = 0.01
+    d, f = on_gpu(c), {k: f64(v) for k, v in c.items()}
+    got, final = ssd.selective_scan_fwd(*args(d), None, d["init"])
+    ref, fref = O.selective_scan(*args(f), None, f["init"])
+    check("y", got, ref)
+    check("final", final, fref)
+
+
+@pytest.mark.parametrize("b,D,N,G,io,y,state,gate,skip,extra", [
+    (3, 24, 16, 1, F, F, F, True, True, 0),
+    (5, 272, 16, 2, B, B, F, True, True, 40),
+    (2, 16, 24, 1, B, F, F, False, False, 0),
+    (2, 24, 128, 1, F, F, F, True, True, 8),
+    (1, 8, 200, 1, F, F, F, True, True, 0),
+    (9, 40, 8, 1, B, B, F, True, True, 0),
+])
+def test_selective_state_update_is_the_scan_token_by_token(b, D, N, G, io, y, state, gate, skip, extra):
+    L = 5
+    c = case(b, L, D, N, G, io, state, True, gate, skip, 500 + D)
+    f = {k: f64(v) for k, v in c.items()}
+    ref, fref = O.selective_scan(*args(f), f["z"], f["init"])
+    d = on_gpu(c, extra)
+    st = d["init"].clone()
+    for i in range(L):
+        tok = {k: v[:, i].contiguous() if k in ("x", "dt_raw", "B", "C") else v for k, v in d.items()}
+        got = ssd.selective_state_update(st, *args(tok), None if d["z"] is None else d["z"][:, i], y_dtype=t_dtype(y))
+        check(f"y of token {i}", got, ref[:, i])
+    check("state", st, fref)
+
+
+def test_selective_state_update_bf16_state_rounds_once():
+    c = case(4, None, 40, 16, 1, B, B, True, True, True, 11)
+    f = {k: f64(v) for k, v in c.items()}
+    d = on_gpu(c)
+    h, y = O.selective_step(f["init"], f["x"], f["dt_raw"], f["dt_bias"], f["A"], f["B"], f["C"], f["D"], f["z"])
+    st = d["init"]
+    got = ssd.selective_state_update(st, *args(d), d["z"], y_dtype=torch().float32)
+    check("y", got, y)                         # y reads the state before its rounding
+    check("state", st, h)
+
+
+@pytest.mark.parametrize("b,L,D,N,G,io,g,state,init,gate,skip,dfinal,extra", [
+    (2, 37, 24, 16, 1, F, F, F, True, True, True, True, 0),
+    (2, 70, 72, 16, 1, B, B, F, False, True, True, False, 24),
+    (1, 300, 136, 8, 1, F, F, F, True, False, True, True, 0),
+    (2, 33, 48, 24, 2, B, F, B, True, True, True, True, 8),
+    (1, 65, 16, 64, 2, F, F, F, True, True, True, True, 0),
+    (2, 40, 24, 128, 1, B, B, F, True, False, False, True, 0),
+    (1, 20, 16, 136, 1, F, F, F, True, True, True, True, 0),
+    (1, 19, 8, 256, 1, F, F, F, False, True, True, True, 0),
+    (1, 1100, 8, 16, 1, F, F, F, True, True, True, True, 0),
+    (2, 16, 200, 16, 1, F, F, F, True, True, True, True, 0),             # one chunk exactly
+    (2, 1, 16, 16, 1, B, B, B, True, True, True, True, 0),
+    (2, 0, 16, 16, 1, F, F, F, True, True, True, True, 0),
+    (0, 4, 16, 16, 1, F, F, F, False, False, True, False, 0),
+])
+def test_selective_scan_bwd(b, L, D, N, G, io, g, state, init, gate, skip, dfinal, extra):
+    c = case(b, L, D, N, G, io, state, init, gate, skip, 600 + L + N)
+    dy = draw([13, L], (b, L, D), io)
+    df = draw([14, L], (b, D, N), state, 0.5) if dfinal else None
+    d, f = on_gpu(c, extra), {k: f64(v) for k, v in c.items()}
+    got = ssd.selective_scan_bwd(*args(d), to_dev(dy), d["z"], d["init"], dev(df), grad_dtype=t_dtype(g),
+                                 state_dtype=t_dtype(state))
+    ref = O.selective_scan_bwd(*args(f), f["z"], f["init"], f64(dy), f64(df))
+    if not skip:
+        ref["ddt_bias"] = ref["dD"] = None
+    check_dict(got, ref)
+
+
+def test_selective_scan_bwd_repeats_bit_for_bit():
+    t = torch()
+    c = case(2, 100, 136, 16, 1, B, F, True, True, True, 15)
+    d, dy = on_gpu(c), to_dev(draw(16, (2, 100, 136), B))
+    outs = [ssd.selective_scan_bwd(*args(d), dy, d["z"], d["init"]) for _ in range(2)]
+    for k in outs[0]:
+        assert t.equal(outs[0][k], outs[1][k]), k
+
+
+def test_gradients_against_differences_of_the_forward_kernel():
+    """Directional differences of the fp32 forward kernel's own outputs, weighted in 64 bits: with a step
+    of 2^-6 the second-order term cancels, the third is below 2^-12 of the scale and the outputs' rounding
+    (2^-22 of the sum of |y dy|, over 2^-5) below 2^-17: 2^-9 of the scale holds both."""
+    t = torch()
+    c = case(1, 40, 16, 16, 1, F, F, True, True, True, 21)
+    dy, df = draw(22, (1, 40, 16), F), draw(23, (1, 16, 16), F)
+    d = on_gpu(c)
+    g = ssd.selective_scan_bwd(*args(d), to_dev(dy), d["z"], d["init"], to_dev(df))
+    names = ("x", "dt_raw", "dt_bias", "A", "B", "C", "D", "z", "init")
+    grads = dict(zip(names, (g[k] for k in ("dx", "ddt_raw", "ddt_bias", "dA", "dB", "dC", "dD", "dz", "dinit_state"))))
+    wy, wf = to_dev(dy).double(), to_dev(df).double()
+
+    def loss(e):
+        y, f = ssd.selective_scan_fwd(*args(e), e["z"].contiguous(), e["init"])
+        return float((y.double() * wy).sum() + (f.double() * wf).sum()), float((y.double() * wy).abs().sum())
+
+    h = 2.0 ** -6
+    for i, k in enumerate(names):
+        step = t.randn(d[k].shape, generator=t.Generator("cuda").manual_seed(i), device="cuda")
+        up, size = loss({**d, k: d[k] + h * step})
+        down, _ = loss({**d, k: d[k] - h * step})
+        num, ana = (up - down) / (2 * h), float((grads[k].double() * step).sum())
+        assert abs(num - ana) <= 2.0 ** -9 * (size + abs(ana)), (k, num, ana, size)
