@@ -21,6 +21,25 @@ namespace ssd {
 
 constexpr int kSbWarps = 4, kSbThreads = kSbWarps * 32;
 
+struct SbShape {
+    int K;            // lanes of a channel
+    int CT;           // channels of a block
+    int Dg, tiles;    // channels of a group, blocks that cover them
+    int Np;           // K * S
+};
+
+template <int S>
+inline SbShape sel_shape(int64_t D, int64_t N, int64_t G, int warps) {
+    SbShape sh{};
+    sh.K = 1;
+    while (sh.K * S < N) sh.K *= 2;
+    sh.Np = sh.K * S;
+    sh.CT = warps * (32 / sh.K) * 2;
+    sh.Dg = (int)(D / G);
+    sh.tiles = (sh.Dg + sh.CT - 1) / sh.CT;
+    return sh;
+}
+
 struct SbLayout {
     int T;                       // tokens of a chunk
     int nch;                     // chunks of a sequence
@@ -37,7 +56,7 @@ static int sb_states(int64_t N) { return N > 128 ? 8 : 4; }
 
 static SbLayout sb_layout(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
     SbLayout l{};
-    const SelShape sh = sb_states(N) == 8 ? sel_shape<8>(D, N, G, kSbWarps) : sel_shape<4>(D, N, G, kSbWarps);
+    const SbShape sh = sb_states(N) == 8 ? sel_shape<8>(D, N, G, kSbWarps) : sel_shape<4>(D, N, G, kSbWarps);
     l.T = sb_states(N) == 8 ? 8 : 16;
     l.nch = (int)((L + l.T - 1) / l.T);
     const int64_t chunks = batch * l.nch * G, want = 148 * 6;
@@ -63,7 +82,7 @@ size_t selective_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, i
 
 // Stages dt, x, g (fp32, zero past the sequence and the group's channels) and B, C of a chunk.
 template <typename IoT>
-__device__ __forceinline__ void sb_stage(const SelectiveArgs& a, const SelShape& sh, int T, int64_t b, int64_t g,
+__device__ __forceinline__ void sb_stage(const SelectiveArgs& a, const SbShape& sh, int T, int64_t b, int64_t g,
                                          int64_t t0, int nt, int64_t d0, int nc, float* sdt, float* sx, float* sg,
                                          float* sB, float* sC) {
     const int CT = sh.CT, Np = sh.Np;
@@ -116,7 +135,7 @@ __device__ __forceinline__ void load_A(const SelectiveArgs& a, int64_t d, bool o
 
 template <typename IoT, int S>
 __global__ void __launch_bounds__(kSbThreads)
-selective_bwd_summary_kernel(const SelectiveArgs a, const SelShape sh, const SbLayout l) {
+selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh, const SbLayout l) {
     extern __shared__ float4 smem4[];
     const int T = l.T, CT = sh.CT, Np = sh.Np, K = sh.K;
     float* sdt = (float*)smem4;
@@ -214,7 +233,7 @@ selective_bwd_chunks_kernel(const SelectiveArgs a, const SbLayout l) {
 
 template <typename IoT, typename GT, int S>
 __global__ void __launch_bounds__(kSbThreads)
-selective_bwd_main_kernel(const SelectiveArgs a, const SelShape sh, const SbLayout l) {
+selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh, const SbLayout l) {
     extern __shared__ float4 smem4[];
     const int T = l.T, CT = sh.CT, Np = sh.Np, K = sh.K;
     float4* hs = smem4;                                // [T][2 S / 4][threads]
@@ -422,7 +441,7 @@ __global__ void selective_bwd_empty_kernel(const SelectiveArgs a) {
 
 template <typename IoT, typename GT, int S>
 static cudaError_t launch_bwd_t(const SelectiveArgs& a, cudaStream_t s) {
-    const SelShape sh = sel_shape<S>(a.D, a.N, a.G, kSbWarps);
+    const SbShape sh = sel_shape<S>(a.D, a.N, a.G, kSbWarps);
     const SbLayout l = sb_layout(a.batch, a.L, a.D, a.N, a.G);
     const int smem1 = (int)sizeof(float) * l.T * (3 * sh.CT + 2 * sh.Np);
     const int smem3 = (int)sizeof(float) * l.T * (2 * S * kSbThreads + kSbWarps * 2 * sh.Np + 6 * sh.CT + 2 * sh.Np);

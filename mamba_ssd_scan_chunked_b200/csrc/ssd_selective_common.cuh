@@ -18,23 +18,110 @@ __device__ __forceinline__ float exp2_approx(float v) {
     return r;
 }
 
-struct SelShape {
-    int K;            // lanes of a channel
-    int CT;           // channels of a block
-    int Dg, tiles;    // channels of a group, blocks that cover them
-    int Np;           // K * S
+// exp(v) for a few values a channel and token: 2^(v log2 e) with the rounding
+// error of that product put back, so that the result is as exact as ex2 (2^-22).
+__device__ __forceinline__ float exp_f32(float v) {
+    const float hi = v * kLog2e;
+    const float lo = fmaf(v, 1.9259629911266175e-8f, fmaf(v, kLog2e, -hi));   // log2 e - fl(log2 e)
+    const float e = exp2_approx(hi);
+    return fmaf(e, lo * 0.6931471805599453f, e);
+}
+
+// softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|) in [0, 1].  log(1 + e) / e
+// is the polynomial of degree 9 that is best in relative error over [0, 1]
+// (5e-9 from its coefficients, 1.1e-7 evaluated in fp32), which keeps the whole
+// relative precision where dt is small; a difference of logarithms would not.
+// Against log1pf(expf(z)) it saves one special function and a branch.
+__device__ __forceinline__ float softplus_poly(float z) {
+    const float e = exp_f32(-fminf(fabsf(z), 200.f));
+    float p = -0.003244024235755205f;
+    p = fmaf(p, e, 0.019851457327604294f);
+    p = fmaf(p, e, -0.056959524750709534f);
+    p = fmaf(p, e, 0.10603653639554977f);
+    p = fmaf(p, e, -0.15305592119693756f);
+    p = fmaf(p, e, 0.1967593878507614f);
+    p = fmaf(p, e, -0.24954134225845337f);
+    p = fmaf(p, e, 0.3332996368408203f);
+    p = fmaf(p, e, -0.4999990165233612f);
+    p = fmaf(p, e, 1.f);
+    float m;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m) : "f"(z));   // NaN stays NaN
+    return fmaf(p, e, m);
+}
+
+// 8 elements as they lie in memory, widened when they are used
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float* v) const { Vec16<bf16>::unpack(r, v); }
+};
+template <> struct Raw8<float> {
+    uint4 r[2];
+    __device__ __forceinline__ void load(const float* p) {
+        r[0] = *reinterpret_cast<const uint4*>(p);
+        r[1] = *reinterpret_cast<const uint4*>(p + 4);
+    }
+    __device__ __forceinline__ void zero() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float* v) const {
+        Vec16<float>::unpack(r[0], v);
+        Vec16<float>::unpack(r[1], v + 4);
+    }
 };
 
-template <int S>
-inline SelShape sel_shape(int64_t D, int64_t N, int64_t G, int warps) {
-    SelShape sh{};
-    sh.K = 1;
-    while (sh.K * S < N) sh.K *= 2;
-    sh.Np = sh.K * S;
-    sh.CT = warps * (32 / sh.K) * 2;
-    sh.Dg = (int)(D / G);
-    sh.tiles = (sh.Dg + sh.CT - 1) / sh.CT;
-    return sh;
+// Lanes and channels: lane = state group * (32 / K) + pair, so that the lanes
+// that read the same B and C are neighbours (a 16-byte shared load then takes 2
+// cycles of an SM, 4 when every fourth lane reads the same, measured).
+template <int K_, int S_, int W_>
+struct SelTile {
+    static constexpr int K = K_;             // lanes of a channel
+    static constexpr int S = S_;             // states of a lane
+    static constexpr int W = W_;             // warps of a block
+    static constexpr int Np = K * S;         // states with padding
+    static constexpr int P = 32 / K;         // pairs of channels of a warp
+    static constexpr int CT = W * P * 2;     // channels of a block
+};
+
+struct SelShape {
+    int Dg, tiles;           // channels of a group, blocks that cover them
+    int nch, clen;           // chunks of a sequence and their tokens
+};
+
+// Sums v[i] over the K lanes of a channel (xor distances P, 2 P, .. 16); lane
+// group k of the K ends up with the sums of values first(k) .. first(k) + 8 / K
+// (8 / K >= 1), or, with K > 8, each value is on several lanes.
+template <int K>
+__device__ __forceinline__ int sum_over_states(float (&v)[8], int lane) {
+    constexpr int P = 32 / K;
+    int first = 0;
+    if constexpr (K >= 2) {
+        const bool up = lane & P;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float send = up ? v[i] : v[i + 4], keep = up ? v[i + 4] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, P);
+        }
+        first += up ? 4 : 0;
+    }
+    if constexpr (K >= 4) {
+        const bool up = lane & (2 * P);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float send = up ? v[i] : v[i + 2], keep = up ? v[i + 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * P);
+        }
+        first += up ? 2 : 0;
+    }
+    if constexpr (K >= 8) {
+        const bool up = lane & (4 * P);
+        const float send = up ? v[0] : v[1], keep = up ? v[1] : v[0];
+        v[0] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * P);
+        first += up ? 1 : 0;
+    }
+#pragma unroll
+    for (int o = 8 * P; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    return first;
 }
 
 }  // namespace ssd
