@@ -132,7 +132,7 @@ typedef struct {
 /* Short causal convolution problem description. */
 typedef struct {
     int64_t batch;      /* >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
-    int64_t seqlen;     /* >= 0; 0 writes final_state = init_state (or zeros); 1 for ssd_conv1d_update */
+    int64_t seqlen;     /* >= 0, <= 2^30; 0 writes final_state = init_state (or zeros); 1 for ssd_conv1d_update */
     int64_t channels;   /* multiple of 8, <= 2^20 */
     int64_t width;      /* taps: 2, 3 or 4 */
     int64_t x_stride;   /* elements from a token's row of x to the next: >= channels, multiple of 8 */
@@ -148,7 +148,8 @@ typedef struct {
 /* Selective scan problem description (a decay per channel and state). */
 typedef struct {
     int64_t batch;      /* >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
-    int64_t seqlen;     /* >= 0; 0 writes final_state = init_state (or zeros); 1 for ssd_selective_state_update */
+    int64_t seqlen;     /* >= 0, <= 2^30; 0 writes final_state = init_state (or zeros); 1 for
+                           ssd_selective_state_update */
     int64_t channels;   /* D; channels / ngroups is a multiple of 8; <= 2^20 */
     int64_t dstate;     /* N, multiple of 8, <= 256 */
     int64_t ngroups;    /* G >= 1: channel d uses group d / (D / G) of B and C */

@@ -48,7 +48,7 @@ static size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, size_t e) 
 }
 
 constexpr int64_t kMaxChannels = (int64_t)1 << 20, kMaxStride = (int64_t)1 << 24;
-constexpr int64_t kMaxBatch = (int64_t)1 << 24, kMaxLen = (int64_t)1 << 31, kMaxBlocks = (int64_t)1 << 31;
+constexpr int64_t kMaxBatch = (int64_t)1 << 24, kMaxLen = (int64_t)1 << 30, kMaxBlocks = (int64_t)1 << 31;
 
 static ssd_status_t check_conv1d_desc(const ssd_conv1d_desc_t* d, bool backward) {
     if (!d) return SSD_ERR_INVALID_ARG;

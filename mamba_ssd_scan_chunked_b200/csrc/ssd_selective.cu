@@ -23,19 +23,19 @@ namespace ssd {
 // the last from 0 and the sum of its dt, selective_chunks_kernel the state that
 // enters each, and the main pass starts from it.
 template <typename IoT, typename YT, class Tile, int T, bool SUMMARY>
-__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 4 ? 4 : 2)
+__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 8 ? 2 : 1)
 selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict__ wstate, float* __restrict__ wdt) {
     constexpr int K = Tile::K, S = Tile::S, Np = Tile::Np, P = Tile::P, CT = Tile::CT, THREADS = Tile::W * 32;
     constexpr int V = CT / 8;                                   // 8-channel vectors of a token here
     constexpr int IT = (T * V + THREADS - 1) / THREADS;         // of a thread in a tile
     constexpr int BN = T * Np / 8;                              // 8-state vectors of a tile's B
     constexpr int IB = ((SUMMARY ? 1 : 2) * BN + THREADS - 1) / THREADS;
-    constexpr int YS = CT % 32 == 0 ? CT + 16 : CT;             // row of y: no bank conflict between 4 tokens
+    constexpr int YS = CT + 4;                                  // row of y: 8 tokens' values meet all banks
     extern __shared__ float4 smem4[];
-    float4* sd = smem4;                                         // [2][T][CT / 2]: dt, dt, dt x, dt x
+    float4* sd = smem4;                                         // [2][T][CT / 2]: (dt, dt x) of two channels
     float* sB = (float*)(sd + 2 * T * (CT / 2));                // [2][T][Np]
     float* sC = sB + 2 * T * Np;                                // [2][T][Np]
-    float* sy = sC + (SUMMARY ? 0 : 2 * T * Np);                // [T][YS]
+    float* sy = sC + (SUMMARY ? 0 : 2 * T * Np);                // [8 + T][YS]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t nch = SUMMARY ? sh.nch - 1 : sh.nch;
     int64_t r = blockIdx.x;
@@ -50,25 +50,30 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
     int64_t p = a.pad_left ? a.pad_left[b] : 0;
     p = p < 0 ? 0 : p > a.L ? a.L : p;
 
-    const int pair = warp * P + lane % P, n0 = (lane / P) * S, ch = pair * 2;
-    const int slot = pair ^ ((pair >> 3) & 7);                  // where the pair lies in a row of sd (see stage)
-    float A2[2][S], h[2][S], sum[2] = {0.f, 0.f};
+    const int ch = warp * P + lane % P, n0 = (lane / P) * S;
+    const bool cok = ch < nc;
+    const int slot = (ch >> 1) ^ ((ch >> 4) & 7);               // where its pair lies in a row of sd (see stage)
+    f32x2 A2[S / 2], h[S / 2];                                  // states s, s + 1
+    float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int s2 = 0; s2 < S / 2; ++s2) {
+        float Av[2] = {0.f, 0.f}, hv[2] = {0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const bool ok = ch + e < nc && n0 + s < a.N;
-            const int64_t i = (d0 + ch + e) * a.N + n0 + s;
-            A2[e][s] = ok ? a.A[i] * kLog2e : 0.f;
-            h[e][s] = 0.f;
-            if (!SUMMARY && ok) {
+        for (int q = 0; q < 2; ++q) {
+            const int s = 2 * s2 + q;
+            const int64_t i = (d0 + ch) * a.N + n0 + s;
+            if (cok && n0 + s < a.N) {
+                Av[q] = a.A[i] * kLog2e;
                 const int64_t k = b * a.D * a.N + i;
-                if (ck > 0) h[e][s] = wstate[(b * (nch - 1) + ck - 1) * a.D * a.N + i];
-                else if (a.init) h[e][s] = a.state_bf16 ? to_f32(((const bf16*)a.init)[k]) : ((const float*)a.init)[k];
+                if (SUMMARY) continue;
+                if (ck > 0) hv[q] = wstate[(b * (nch - 1) + ck - 1) * a.D * a.N + i];
+                else if (a.init) hv[q] = a.state_bf16 ? to_f32(((const bf16*)a.init)[k]) : ((const float*)a.init)[k];
             }
         }
+        A2[s2] = f2_pack(Av[0], Av[1]);
+        h[s2] = f2_pack(hv[0], hv[1]);
+    }
 
-    const int64_t tok0 = b * a.L;
     const int vt = tid / V, vc = (tid % V) * 8;                 // this thread's first token and its channels
     const bool vok = vc < nc;
     float bias[8], Dv[8];
@@ -80,49 +85,61 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
     }
     Raw8<IoT> rx[IT], rdt[IT], rb[IB], rz[IT], nx[IT];
 
-    // raw x, dt, B, C of the tile at t0; tokens before the sequence's first and past the run are absent
-    auto load = [&](int64_t t0) {
+    // addresses of this thread's first token; a tile's tokens of it are STEP apart
+    constexpr int STEP = THREADS / V;
+    const int64_t tok = b * a.L + tb + vt;
+    const IoT* px = (const IoT*)a.x + tok * a.D + d0 + vc;
+    const IoT* pdt = (const IoT*)a.dt_raw + tok * a.D + d0 + vc;
+    const IoT* pz = (const IoT*)a.z + tok * a.zs + d0 + vc;
+    YT* py = (YT*)a.y + tok * a.D + d0 + vc;
+    // and of its vectors of B and C (the halves of a tile's 2 BN vectors)
+    const IoT* pbc[IB];
+    int bct[IB];                                                // token in the tile, or out of every run
+#pragma unroll
+    for (int q = 0; q < IB; ++q) {
+        int i = tid + q * THREADS;
+        const bool second = !SUMMARY && i >= BN;
+        i -= second ? BN : 0;
+        const int t = i / (Np / 8), n = (i % (Np / 8)) * 8;
+        bct[q] = i < BN && n < a.N ? t : 1 << 30;
+        pbc[q] = (const IoT*)(second ? a.C : a.B) + ((b * a.L + tb + t) * a.G + g) * a.N + n;
+    }
+
+    // raw x, dt, B, C of the tile that starts `at` tokens into the run; absent tokens (padding, or past
+    // the run) get x = 0 and dt_raw = -inf, so dt = 0
+    const int len = (int)(te - tb), lead = p <= tb ? 0 : p - tb < len ? (int)(p - tb) : len;
+    auto load = [&](int at) {
 #pragma unroll
         for (int q = 0; q < IT; ++q) {
-            const int t = vt + q * (THREADS / V);
-            const int64_t tt = t0 + t;
+            const int t = vt + q * STEP;
             nx[q].zero();
-            rdt[q].zero();
-            if (vok && t < T && tt >= p && tt < te) {
-                nx[q].load((const IoT*)a.x + (tok0 + tt) * a.D + d0 + vc);
-                rdt[q].load((const IoT*)a.dt_raw + (tok0 + tt) * a.D + d0 + vc);
+            rdt[q].minus_inf();
+            if (vok && t < T && at + t >= lead && at + t < len) {
+                nx[q].load(px + (int64_t)(at + q * STEP) * a.D);
+                rdt[q].load(pdt + (int64_t)(at + q * STEP) * a.D);
             }
         }
 #pragma unroll
         for (int q = 0; q < IB; ++q) {
-            int i = tid + q * THREADS;
-            const bool second = !SUMMARY && i >= BN;
-            i -= second ? BN : 0;
-            const int t = i / (Np / 8), n = (i % (Np / 8)) * 8;
-            const int64_t tt = t0 + t;
             rb[q].zero();
-            if (i < BN && n < a.N && tt >= p && tt < te)
-                rb[q].load((const IoT*)(second ? a.C : a.B) + ((tok0 + tt) * a.G + g) * a.N + n);
+            if (at + bct[q] >= lead && at + bct[q] < len) rb[q].load(pbc[q] + (int64_t)at * (a.G * a.N));
         }
     };
-    auto stage = [&](int64_t t0, int buf) {
+    auto stage = [&](int buf) {
 #pragma unroll
         for (int q = 0; q < IT; ++q) {
-            const int t = vt + q * (THREADS / V);
+            const int t = vt + q * STEP;
             if (t >= T) continue;
-            const int64_t tt = t0 + t;
-            float x[8], dt[8];
+            float x[8], z[8];
             nx[q].get(x);
-            rdt[q].get(dt);
-            const bool live = vok && tt >= p && tt < te;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dt[j] = live ? softplus_poly(dt[j] + bias[j]) : 0.f;
+            rdt[q].get(z);
             // pair k lies at k ^ (k >> 3): 8 threads' vectors, 4 pairs apart, then meet all banks
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int k = vc / 2 + j;
+                const float2 dt = f2_get(softplus2(z[2 * j] + bias[2 * j], z[2 * j + 1] + bias[2 * j + 1]));
                 sd[(buf * T + t) * (CT / 2) + (k ^ ((k >> 3) & 7))] =
-                    make_float4(dt[2 * j], dt[2 * j + 1], dt[2 * j] * x[2 * j], dt[2 * j + 1] * x[2 * j + 1]);
+                    make_float4(dt.x, dt.x * x[2 * j], dt.y, dt.y * x[2 * j + 1]);
             }
         }
 #pragma unroll
@@ -137,80 +154,75 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
         }
     };
 
-    if (tb < te) {
-        load(tb);
-        stage(tb, 0);
+    if (len > 0) {
+        load(0);
+        stage(0);
         __syncthreads();
     }
     int buf = 0;
-    for (int64_t t0 = tb; t0 < te; t0 += T, buf ^= 1) {
+    for (int at = 0; at < len; at += T, buf ^= 1) {
 #pragma unroll
         for (int q = 0; q < IT; ++q) rx[q] = nx[q];
         if (!SUMMARY && a.z) {
 #pragma unroll
             for (int q = 0; q < IT; ++q) {
-                const int t = vt + q * (THREADS / V);
+                const int t = vt + q * STEP;
                 rz[q].zero();
-                if (vok && t < T && t0 + t >= p && t0 + t < te)
-                    rz[q].load((const IoT*)a.z + (tok0 + t0 + t) * a.zs + d0 + vc);
+                if (vok && t < T && at + t >= lead && at + t < len) rz[q].load(pz + (int64_t)(at + q * STEP) * a.zs);
             }
         }
-        if (t0 + T < te) load(t0 + T);
+        if (at + T < len) load(at + T);
         // tokens past the end have dt = 0 and leave the state alone
-        const int nt = te - t0 < T ? (int)(te - t0) : T;
-        const float4* pd = sd + buf * T * (CT / 2) + slot;
+        const int nt = len - at < T ? len - at : T;
+        const float2* pd = (const float2*)(sd + buf * T * (CT / 2) + slot) + (ch & 1);
         const float *pB = sB + buf * T * Np + n0, *pC = sC + buf * T * Np + n0;
-        for (int t = 0; t < nt; t += 4) {
-            float y[8];
+        // 8 tokens a round; the sums over the states of a round are formed in the next one, beside its
+        // exponentials (the first round's stand-in goes to the 8 rows before the tile's)
+        float y[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float4 d = pd[(t + u) * (CT / 2)];
-                float B[S], C[S];
+        for (int i = 0; i < 8; ++i) y[i] = 0.f;
+        auto reduce = [&](int t) {
+            const int first = sum_over_states<K>(y, lane);
+            float* out = sy + (t + 8 + first) * YS + ch;
+            if (K > 8 && lane >= 8 * P) return;
 #pragma unroll
-                for (int s = 0; s < S; s += 4) {
-                    Vec16<float>::load(pB + (t + u) * Np + s, B + s);
-                    if (!SUMMARY) Vec16<float>::load(pC + (t + u) * Np + s, C + s);
+            for (int i = 0; i < (K >= 8 ? 1 : 8 / K); ++i) out[i * YS] = y[i];
+        };
+        for (int t = 0; t < nt; t += 8) {
+            float yn[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float2 d = pd[(t + u) * CT];
+                f32x2 B[S / 2], C[S / 2];
+                f2_load<S>(pB + (t + u) * Np, B);
+                if (!SUMMARY) f2_load<S>(pC + (t + u) * Np, C);
+                const f32x2 dt = f2_pack(d.x, d.x), dx = f2_pack(d.y, d.y);
+                f32x2 ys = 0;
+#pragma unroll
+                for (int s = 0; s < S / 2; ++s) {
+                    h[s] = f2_fma(f2_exp2(f2_mul(dt, A2[s])), h[s], f2_mul(dx, B[s]));
+                    if (!SUMMARY) ys = s ? f2_fma(C[s], h[s], ys) : f2_mul(C[s], h[s]);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float dt = e ? d.y : d.x, dx = e ? d.w : d.z;
-                    float ys = 0.f;
-#pragma unroll
-                    for (int s = 0; s < S; ++s) {
-                        h[e][s] = fmaf(exp2_approx(dt * A2[e][s]), h[e][s], dx * B[s]);
-                        if (!SUMMARY) ys = fmaf(C[s], h[e][s], ys);
-                    }
-                    y[u * 2 + e] = ys;
-                    if (SUMMARY) sum[e] += dt;
-                }
+                const float2 yy = f2_get(ys);
+                yn[u] = yy.x + yy.y;
+                if (SUMMARY) sum += d.x;
             }
             if constexpr (!SUMMARY) {
-                // lane group 8 / K values further: value 2 u + e is token u, channel e
-                const int first = sum_over_states<K>(y, lane);
-                float* out = sy + (t + first / 2) * YS + ch;
-                if constexpr (K == 1) {
+                reduce(t - 8);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) *(float2*)(out + u * YS) = make_float2(y[2 * u], y[2 * u + 1]);
-                } else if constexpr (K == 2) {
-                    *(float2*)out = make_float2(y[0], y[1]);
-                    *(float2*)(out + YS) = make_float2(y[2], y[3]);
-                } else if constexpr (K == 4) {
-                    *(float2*)out = make_float2(y[0], y[1]);
-                } else {
-                    if (lane < 8 * P) out[first & 1] = y[0];
-                }
+                for (int i = 0; i < 8; ++i) y[i] = yn[i];
             }
         }
+        if constexpr (!SUMMARY) reduce((nt - 1) & ~7);
         __syncthreads();                                        // sy is complete, this tile's buffer free
         if constexpr (!SUMMARY) {
 #pragma unroll
             for (int q = 0; q < IT; ++q) {
-                const int t = vt + q * (THREADS / V);
-                const int64_t tt = t0 + t;
-                if (!vok || t >= T || tt >= te) continue;
+                const int t = vt + q * STEP;
+                if (!vok || t >= T || at + t >= len) continue;
                 float x[8], y[8];
                 rx[q].get(x);
-                load8(sy + t * YS + vc, y);
+                load8(sy + (t + 8) * YS + vc, y);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = fmaf(Dv[j], x[j], y[j]);
                 if (a.z) {
@@ -219,35 +231,29 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] *= z[j] * sigmoid_f32(z[j]);
                 }
-                if (tt < p)
+                if (at < lead && at + t < lead) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = 0.f;
-                store8((YT*)a.y + (tok0 + tt) * a.D + d0 + vc, y);
+                }
+                store8(py + (int64_t)(at + q * STEP) * a.D, y);
             }
         }
-        if (t0 + T < te) stage(t0 + T, buf ^ 1);
+        if (at + T < len) stage(buf ^ 1);
         __syncthreads();                                        // the next tile is ready, sy free
     }
-    if (SUMMARY) {
-        const int64_t bc = b * nch + ck;
+    if (!cok) return;
+    const int64_t bc = b * nch + ck;
+    if (SUMMARY && n0 == 0) wdt[bc * a.D + d0 + ch] = sum;
+    if (!SUMMARY && !(a.final_state && ck == nch - 1)) return;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (ch + e >= nc) continue;
-            if (n0 == 0) wdt[bc * a.D + d0 + ch + e] = sum[e];
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (n0 + s < a.N) wstate[(bc * a.D + d0 + ch + e) * a.N + n0 + s] = h[e][s];
-        }
-    } else if (a.final_state && ck == nch - 1) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (ch + e < nc && n0 + s < a.N) {
-                    const int64_t k = b * a.D * a.N + (d0 + ch + e) * a.N + n0 + s;
-                    if (a.state_bf16) ((bf16*)a.final_state)[k] = from_f32<bf16>(h[e][s]);
-                    else ((float*)a.final_state)[k] = h[e][s];
-                }
+    for (int s = 0; s < S; ++s) {
+        if (n0 + s >= a.N) continue;
+        const float2 hv = f2_get(h[s / 2]);
+        const float v = s & 1 ? hv.y : hv.x;
+        const int64_t i = (d0 + ch) * a.N + n0 + s;
+        if (SUMMARY) wstate[bc * a.D * a.N + i] = v;
+        else if (a.state_bf16) ((bf16*)a.final_state)[b * a.D * a.N + i] = from_f32<bf16>(v);
+        else ((float*)a.final_state)[b * a.D * a.N + i] = v;
     }
 }
 
@@ -310,7 +316,7 @@ selective_update_kernel(const SelectiveArgs a, int K, int per_block) {
 // block where a warp covers few channels, so that a token's row stays whole vectors.
 constexpr int kSelMaxChunks = 64;
 
-static int tile_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : N <= 64 ? 32 : 16; }
+static int tile_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 static int tile_tokens(int64_t N) { return N > 128 ? 16 : 32; }
 
 // A block's warps each keep one of the SM's four special function units busy, two
@@ -353,8 +359,8 @@ template <typename IoT, typename YT, class Tile, int T>
 static cudaError_t launch_fwd_t(const SelectiveArgs& a, cudaStream_t s) {
     constexpr int CT = Tile::CT, Np = Tile::Np, THREADS = Tile::W * 32;
     const SelShape sh = sel_shape(a.batch, a.L, a.D, a.N, a.G);
-    constexpr int YS = CT % 32 == 0 ? CT + 16 : CT;
-    constexpr int smem = (int)sizeof(float) * T * (4 * CT + 4 * Np + YS), smem1 = (int)sizeof(float) * T * (4 * CT + 2 * Np);
+    constexpr int YS = CT + 4;
+    constexpr int smem = (int)sizeof(float) * (T * (4 * CT + 4 * Np + YS) + 8 * YS), smem1 = (int)sizeof(float) * T * (4 * CT + 2 * Np);
     const auto main = selective_fwd_kernel<IoT, YT, Tile, T, false>;
     const auto summary = selective_fwd_kernel<IoT, YT, Tile, T, true>;
     cudaError_t e = cudaSuccess;
@@ -375,12 +381,12 @@ static cudaError_t launch_fwd_t(const SelectiveArgs& a, cudaStream_t s) {
 
 template <typename IoT, typename YT>
 static cudaError_t launch_fwd_s(const SelectiveArgs& a, cudaStream_t s) {
-    if (a.N <= 8) return launch_fwd_t<IoT, YT, SelTile<2, 4, 4>, 32>(a, s);
-    if (a.N <= 16) return launch_fwd_t<IoT, YT, SelTile<4, 4, 4>, 32>(a, s);
-    if (a.N <= 32) return launch_fwd_t<IoT, YT, SelTile<8, 4, 4>, 32>(a, s);
+    if (a.N <= 8) return launch_fwd_t<IoT, YT, SelTile<2, 4, 8>, 32>(a, s);
+    if (a.N <= 16) return launch_fwd_t<IoT, YT, SelTile<4, 4, 8>, 32>(a, s);
+    if (a.N <= 32) return launch_fwd_t<IoT, YT, SelTile<8, 4, 8>, 32>(a, s);
     if (a.N <= 64) return launch_fwd_t<IoT, YT, SelTile<16, 4, 8>, 32>(a, s);
-    if (a.N <= 128) return launch_fwd_t<IoT, YT, SelTile<32, 4, 8>, 32>(a, s);
-    return launch_fwd_t<IoT, YT, SelTile<32, 8, 8>, 16>(a, s);
+    if (a.N <= 128) return launch_fwd_t<IoT, YT, SelTile<32, 4, 16>, 32>(a, s);
+    return launch_fwd_t<IoT, YT, SelTile<32, 8, 16>, 16>(a, s);
 }
 
 cudaError_t launch_selective_fwd(const SelectiveArgs& a, cudaStream_t s) {

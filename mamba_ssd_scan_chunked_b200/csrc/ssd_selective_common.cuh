@@ -18,35 +18,67 @@ __device__ __forceinline__ float exp2_approx(float v) {
     return r;
 }
 
-// exp(v) for a few values a channel and token: 2^(v log2 e) with the rounding
-// error of that product put back, so that the result is as exact as ex2 (2^-22).
-__device__ __forceinline__ float exp_f32(float v) {
-    const float hi = v * kLog2e;
-    const float lo = fmaf(v, 1.9259629911266175e-8f, fmaf(v, kLog2e, -hi));   // log2 e - fl(log2 e)
-    const float e = exp2_approx(hi);
-    return fmaf(e, lo * 0.6931471805599453f, e);
+// Two fp32 operations in one instruction (neighbouring states of a lane): the
+// rate of the arithmetic is the same, the issue slots are halved.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 f2_pack(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_exp2(f32x2 v) {
+    const float2 t = f2_get(v);
+    return f2_pack(exp2_approx(t.x), exp2_approx(t.y));
+}
+// S consecutive floats (16-byte aligned) as S / 2 pairs
+template <int S> __device__ __forceinline__ void f2_load(const float* p, f32x2 (&v)[S / 2]) {
+#pragma unroll
+    for (int i = 0; i < S / 4; ++i) {
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(p + 4 * i);
+        v[2 * i] = r.x;
+        v[2 * i + 1] = r.y;
+    }
 }
 
-// softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|) in [0, 1].  log(1 + e) / e
-// is the polynomial of degree 9 that is best in relative error over [0, 1]
-// (5e-9 from its coefficients, 1.1e-7 evaluated in fp32), which keeps the whole
-// relative precision where dt is small; a difference of logarithms would not.
-// Against log1pf(expf(z)) it saves one special function and a branch.
-__device__ __forceinline__ float softplus_poly(float z) {
-    const float e = exp_f32(-fminf(fabsf(z), 200.f));
-    float p = -0.003244024235755205f;
-    p = fmaf(p, e, 0.019851457327604294f);
-    p = fmaf(p, e, -0.056959524750709534f);
-    p = fmaf(p, e, 0.10603653639554977f);
-    p = fmaf(p, e, -0.15305592119693756f);
-    p = fmaf(p, e, 0.1967593878507614f);
-    p = fmaf(p, e, -0.24954134225845337f);
-    p = fmaf(p, e, 0.3332996368408203f);
-    p = fmaf(p, e, -0.4999990165233612f);
-    p = fmaf(p, e, 1.f);
-    float m;
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m) : "f"(z));   // NaN stays NaN
-    return fmaf(p, e, m);
+// softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|) in [0, 1], of two values.
+// log(1 + e) / e is the polynomial of degree 9 that is best in relative error
+// over [0, 1] (5e-9 from its coefficients, 1.1e-7 evaluated in fp32), which keeps
+// the whole relative precision where dt is small; a difference of logarithms
+// would not.  Against log1pf(expf(z)) it saves one special function and a branch.
+// -inf gives 0, NaN stays NaN.
+__device__ __forceinline__ f32x2 softplus2(float z0, float z1) {
+    const f32x2 v = f2_pack(-fminf(fabsf(z0), 200.f), -fminf(fabsf(z1), 200.f));
+    // exp(v) = 2^(v log2 e) with the rounding error of that product put back
+    const f32x2 L = f2_pack(kLog2e, kLog2e), hi = f2_mul(v, L);
+    const f32x2 err = f2_fma(v, L, f2_mul(hi, f2_pack(-1.f, -1.f)));
+    const f32x2 lo = f2_fma(v, f2_pack(1.9259629911266175e-8f, 1.9259629911266175e-8f), err);   // log2 e - fl(log2 e)
+    const f32x2 e0 = f2_exp2(hi);
+    const f32x2 e = f2_fma(e0, f2_mul(lo, f2_pack(0.6931471805599453f, 0.6931471805599453f)), e0);
+    constexpr float c[9] = {0.019851457327604294f, -0.056959524750709534f, 0.10603653639554977f,
+                            -0.15305592119693756f, 0.1967593878507614f,    -0.24954134225845337f,
+                            0.3332996368408203f,   -0.4999990165233612f,   1.f};
+    f32x2 p = f2_pack(-0.003244024235755205f, -0.003244024235755205f);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) p = f2_fma(p, e, f2_pack(c[i], c[i]));
+    float m0, m1;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m0) : "f"(z0));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m1) : "f"(z1));
+    return f2_fma(p, e, f2_pack(m0, m1));
 }
 
 // 8 elements as they lie in memory, widened when they are used
@@ -55,6 +87,7 @@ template <> struct Raw8<bf16> {
     uint4 r;
     __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void minus_inf() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ __forceinline__ void get(float* v) const { Vec16<bf16>::unpack(r, v); }
 };
 template <> struct Raw8<float> {
@@ -64,23 +97,28 @@ template <> struct Raw8<float> {
         r[1] = *reinterpret_cast<const uint4*>(p + 4);
     }
     __device__ __forceinline__ void zero() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void minus_inf() {
+        r[0] = r[1] = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+    }
     __device__ __forceinline__ void get(float* v) const {
         Vec16<float>::unpack(r[0], v);
         Vec16<float>::unpack(r[1], v + 4);
     }
 };
 
-// Lanes and channels: lane = state group * (32 / K) + pair, so that the lanes
-// that read the same B and C are neighbours (a 16-byte shared load then takes 2
-// cycles of an SM, 4 when every fourth lane reads the same, measured).
+// Lanes and channels: a lane holds S neighbouring states of one channel, K lanes
+// (a power of two) its N states, padded with A = B = C = 0, which keep a state at
+// 0.  lane = state group * (32 / K) + channel, so that the lanes that read the
+// same B and C are neighbours (a 16-byte shared load then takes 2 cycles of an
+// SM; 4 when every fourth lane reads the same, measured).
 template <int K_, int S_, int W_>
 struct SelTile {
     static constexpr int K = K_;             // lanes of a channel
     static constexpr int S = S_;             // states of a lane
     static constexpr int W = W_;             // warps of a block
     static constexpr int Np = K * S;         // states with padding
-    static constexpr int P = 32 / K;         // pairs of channels of a warp
-    static constexpr int CT = W * P * 2;     // channels of a block
+    static constexpr int P = 32 / K;         // channels of a warp
+    static constexpr int CT = W * P;         // channels of a block
 };
 
 struct SelShape {
