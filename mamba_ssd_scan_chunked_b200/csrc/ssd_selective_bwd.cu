@@ -12,36 +12,39 @@
 //     exponential serves both);
 //  2. recombination over the chunks: the state that enters each chunk, the
 //     adjoint that leaves it (decay of a chunk: exp(A sum dt));
-//  3. per chunk: the states forward, kept in shared memory, then the adjoint
-//     back over them.  A block goes over several tiles of channels and adds dB
-//     and dC up in shared memory; blocks' sums are added in a fixed order last.
+//  3. per chunk: the states forward, every GT-th kept in shared memory, then the
+//     adjoint back in groups of GT tokens, whose decays serve the group's states
+//     and its adjoint.  A block goes over several tiles of channels and adds
+//     their dB and dC up; blocks' sums are added in a fixed order last.
+//
+// Three exponentials for each state of each token and about 130 instructions for
+// every four: bound by the instruction rate and the special function units.
 #include "ssd_selective_common.cuh"
 
 namespace ssd {
 
-constexpr int kSbWarps = 4, kSbThreads = kSbWarps * 32;
-
-struct SbShape {
-    int K;            // lanes of a channel
-    int CT;           // channels of a block
-    int Dg, tiles;    // channels of a group, blocks that cover them
-    int Np;           // K * S
+// A lane of the third step holds S states of 2 channels, so that half of the
+// sums of dB and dC over the channels are formed in registers.
+template <int K_, int S_, int T_, int GT_>
+struct SbTile {
+    static constexpr int K = K_;             // lanes of a channel
+    static constexpr int S = S_;             // states of a lane
+    static constexpr int T = T_;             // tokens of a chunk
+    static constexpr int GT = GT_;           // tokens of a group of the way back
+    static constexpr int W = 4;              // warps of a block
+    static constexpr int THREADS = W * 32;
+    static constexpr int Np = K * S;
+    static constexpr int P = 32 / K;         // pairs of channels of a warp
+    static constexpr int CT = W * P * 2;     // channels of a block
+    static constexpr int YS = CT + 8;        // row of sy: 4 tokens' pairs meet all banks
+    static constexpr int ACC = (T * Np + THREADS - 1) / THREADS;   // of the chunk's sums of dB (dC) a thread
+    static constexpr int SMEM = (int)sizeof(float) * (T * CT * 3 + T * YS + (T / GT - 1) * 2 * S * THREADS +
+                                                      2 * T * Np + W * T * Np);
 };
 
-template <int S>
-inline SbShape sel_shape(int64_t D, int64_t N, int64_t G, int warps) {
-    SbShape sh{};
-    sh.K = 1;
-    while (sh.K * S < N) sh.K *= 2;
-    sh.Np = sh.K * S;
-    sh.CT = warps * (32 / sh.K) * 2;
-    sh.Dg = (int)(D / G);
-    sh.tiles = (sh.Dg + sh.CT - 1) / sh.CT;
-    return sh;
-}
-
-struct SbLayout {
-    int T;                       // tokens of a chunk
+struct SbShape {
+    int Dg, tiles;               // channels of a group, tiles that cover them
+    int tiles1;                  // the same with the tiles of the summaries
     int nch;                     // chunks of a sequence
     int split;                   // blocks that share a chunk's tiles of channels
     size_t off_h, off_g;         // fp32 [b][nch][D][N] chunk states, then adjoints
@@ -52,16 +55,22 @@ struct SbLayout {
     size_t total;
 };
 
-static int sb_states(int64_t N) { return N > 128 ? 8 : 4; }
+static int sb_tokens(int64_t N) { return N <= 8 ? 16 : N <= 32 ? 32 : N <= 128 ? 16 : 8; }
+static int sb_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : N <= 64 ? 16 : 8; }
+static int sum_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : N <= 128 ? 16 : 8; }
 
-static SbLayout sb_layout(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
-    SbLayout l{};
-    const SbShape sh = sb_states(N) == 8 ? sel_shape<8>(D, N, G, kSbWarps) : sel_shape<4>(D, N, G, kSbWarps);
-    l.T = sb_states(N) == 8 ? 8 : 16;
-    l.nch = (int)((L + l.T - 1) / l.T);
-    const int64_t chunks = batch * l.nch * G, want = 148 * 6;
-    l.split = (int)(chunks >= want || chunks == 0 ? 1 : (want + chunks - 1) / chunks);
-    if (l.split > sh.tiles) l.split = sh.tiles;
+static SbShape sb_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
+    SbShape l{};
+    const int T = sb_tokens(N), CT = sb_channels(N), C1 = sum_channels(N);
+    l.Dg = (int)(D / G);
+    l.tiles = (l.Dg + CT - 1) / CT;
+    l.tiles1 = (l.Dg + C1 - 1) / C1;
+    l.nch = (int)((L + T - 1) / T);
+    // 3 blocks an SM; several rounds of them, so that the last one does not leave most SMs idle
+    const int64_t chunks = batch * l.nch * G, want = 148 * 3 * 4;
+    int64_t split = chunks ? (want + chunks - 1) / chunks : 1;
+    if (split > l.tiles) split = l.tiles;
+    l.split = (int)split;
     const auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
     const size_t bn = (size_t)batch * l.nch, st = bn * D * N * sizeof(float);
     l.off_h = 0;
@@ -77,351 +86,530 @@ static SbLayout sb_layout(int64_t batch, int64_t L, int64_t D, int64_t N, int64_
 }
 
 size_t selective_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
-    return batch == 0 || L == 0 ? 0 : sb_layout(batch, L, D, N, G).total;
+    return batch == 0 || L == 0 ? 0 : sb_shape(batch, L, D, N, G).total;
 }
 
-// Stages dt, x, g (fp32, zero past the sequence and the group's channels) and B, C of a chunk.
+// B and C of a chunk in fp32, zero past the sequence
+template <typename IoT, int T, int Np, int THREADS>
+__device__ __forceinline__ void stage_bc(const SelectiveArgs& a, int64_t b, int64_t g, int64_t t0, int nt, float* sB,
+                                         float* sC) {
+    for (int i = threadIdx.x; i < 2 * T * Np / 8; i += THREADS) {
+        const bool second = i >= T * Np / 8;
+        const int k = (second ? i - T * Np / 8 : i) * 8, t = k / Np, n = k % Np;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        if (t < nt && n < a.N) load8((const IoT*)(second ? a.C : a.B) + ((b * a.L + t0 + t) * a.G + g) * a.N + n, v);
+        store8((second ? sC : sB) + k, v);
+    }
+}
+
+// x, dt and g of 8 channels of a token
 template <typename IoT>
-__device__ __forceinline__ void sb_stage(const SelectiveArgs& a, const SbShape& sh, int T, int64_t b, int64_t g,
-                                         int64_t t0, int nt, int64_t d0, int nc, float* sdt, float* sx, float* sg,
-                                         float* sB, float* sC) {
-    const int CT = sh.CT, Np = sh.Np;
-    const int64_t tok0 = b * a.L + t0;
-    for (int i = threadIdx.x; i < T * (CT / 8); i += kSbThreads) {
-        const int t = i / (CT / 8), c = (i % (CT / 8)) * 8;
-        float x[8], dt[8], gy[8];
+__device__ __forceinline__ void load_token(const SelectiveArgs& a, int64_t tok, int64_t d, float (&x)[8], float (&dt)[8],
+                                           float (&g)[8]) {
+    float raw[8], bias[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = dt[j] = gy[j] = 0.f;
-        if (t < nt && c < nc) {
-            const int64_t at = (tok0 + t) * a.D + d0 + c;
-            load8((const IoT*)a.x + at, x);
-            load8((const IoT*)a.dt_raw + at, dt);
-            load8((const IoT*)a.dy + at, gy);
+    for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+    load8((const IoT*)a.x + tok * a.D + d, x);
+    load8((const IoT*)a.dt_raw + tok * a.D + d, raw);
+    load8((const IoT*)a.dy + tok * a.D + d, g);
+    if (a.dt_bias) load8(a.dt_bias + d, bias);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dt[j] = softplus_f32(dt[j] + (a.dt_bias ? a.dt_bias[d0 + c + j] : 0.f));
-            if (a.z) {
-                float z[8];
-                load8((const IoT*)a.z + (tok0 + t) * a.zs + d0 + c, z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) gy[j] *= z[j] * sigmoid_f32(z[j]);
-            }
-        }
-        store8(sdt + t * CT + c, dt);
-        store8(sx + t * CT + c, x);
-        store8(sg + t * CT + c, gy);
+    for (int j = 0; j < 8; j += 2) {
+        const float2 v = f2_get(softplus2(raw[j] + bias[j], raw[j + 1] + bias[j + 1]));
+        dt[j] = v.x;
+        dt[j + 1] = v.y;
     }
-    if (!sB) return;
-    for (int i = threadIdx.x; i < T * Np; i += kSbThreads) {
-        const int t = i / Np, n = i % Np;
-        float bv = 0.f, cv = 0.f;
-        if (t < nt && n < a.N) {
-            const int64_t k = ((tok0 + t) * a.G + g) * a.N + n;
-            bv = to_f32(((const IoT*)a.B)[k]);
-            cv = to_f32(((const IoT*)a.C)[k]);
-        }
-        sB[i] = bv;
-        sC[i] = cv;
+    if (a.z) {
+        float z[8];
+        load8((const IoT*)a.z + tok * a.zs + d, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= z[j] * sigmoid_f32(z[j]);
     }
 }
 
-// loads the lane's A (times log2 e) of 2 channels
+// The S floats of a lane's states n0 .. of row `i` of a matrix [..][N] (zero past N)
 template <int S>
-__device__ __forceinline__ void load_A(const SelectiveArgs& a, int64_t d, bool ok, int n0, float (&A2)[2][S]) {
+__device__ __forceinline__ void load_states(const float* p, int64_t i, int64_t N, int n0, bool ok, f32x2 (&v)[S / 2]) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int s = 0; s < S / 2; ++s) v[s] = 0;
+    if (!ok) return;
 #pragma unroll
-        for (int s = 0; s < S; ++s) A2[e][s] = ok && n0 + s < a.N ? a.A[(d + e) * a.N + n0 + s] * kLog2e : 0.f;
+    for (int s = 0; s < S; s += 4)
+        if (n0 + s < N) {
+            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(p + i * N + n0 + s);
+            v[s / 2] = r.x;
+            v[s / 2 + 1] = r.y;
+        }
+}
+template <int S>
+__device__ __forceinline__ void store_states(float* p, int64_t i, int64_t N, int n0, bool ok, const f32x2 (&v)[S / 2]) {
+    if (!ok) return;
+#pragma unroll
+    for (int s = 0; s < S; s += 4)
+        if (n0 + s < N) *reinterpret_cast<ulonglong2*>(p + i * N + n0 + s) = make_ulonglong2(v[s / 2], v[s / 2 + 1]);
+}
+template <int S>
+__device__ __forceinline__ void times_log2e(f32x2 (&v)[S / 2]) {
+#pragma unroll
+    for (int s = 0; s < S / 2; ++s) v[s] = f2_mul(v[s], f2_pack(kLog2e, kLog2e));
 }
 
-template <typename IoT, int S>
-__global__ void __launch_bounds__(kSbThreads)
-selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh, const SbLayout l) {
+// Step 1 (lanes as in the forward scan: S states of one channel).
+template <typename IoT, class Tile, int T>
+__global__ void __launch_bounds__(Tile::W * 32)
+selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh) {
+    constexpr int S = Tile::S, Np = Tile::Np, CT = Tile::CT, P = Tile::P, THREADS = Tile::W * 32, V = CT / 8;
     extern __shared__ float4 smem4[];
-    const int T = l.T, CT = sh.CT, Np = sh.Np, K = sh.K;
-    float* sdt = (float*)smem4;
-    float* sx = sdt + T * CT;
-    float* sg = sx + T * CT;
-    float* sB = sg + T * CT;
+    float4* sd = smem4;                                  // [T][CT]: dt, dt x, g
+    float* sB = (float*)(sd + T * CT);
     float* sC = sB + T * Np;
-    const int tile = (int)(blockIdx.x % (unsigned)sh.tiles);
-    int64_t r = blockIdx.x / (unsigned)sh.tiles;
+    const int tile = (int)(blockIdx.x % (unsigned)sh.tiles1);
+    int64_t r = blockIdx.x / (unsigned)sh.tiles1;
     const int64_t g = r % a.G;
     r /= a.G;
-    const int64_t ck = r % l.nch, b = r / l.nch, t0 = ck * l.T;
+    const int64_t ck = r % sh.nch, b = r / sh.nch, t0 = ck * T, bc = b * sh.nch + ck;
     const int nt = a.L - t0 < T ? (int)(a.L - t0) : T;
     const int c0 = tile * CT, nc = sh.Dg - c0 < CT ? sh.Dg - c0 : CT;
     const int64_t d0 = g * sh.Dg + c0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int pair = warp * (32 / K) + lane / K, n0 = (lane % K) * S, ch = pair * 2;
+    const int ch = warp * P + lane % P, n0 = (lane / P) * S;
     const bool ok = ch < nc;
-    sb_stage<IoT>(a, sh, T, b, g, t0, nt, d0, nc, sdt, sx, sg, sB, sC);
-    float A2[2][S], h[2][S], P[2][S], Gs[2][S], sum[2] = {0.f, 0.f};
-    load_A<S>(a, d0 + ch, ok, n0, A2);
+    for (int i = threadIdx.x; i < T * V; i += THREADS) {
+        const int t = i / V, c = (i % V) * 8;
+        float x[8], dt[8], gy[8];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+        for (int j = 0; j < 8; ++j) x[j] = dt[j] = gy[j] = 0.f;
+        if (t < nt && c < nc) load_token<IoT>(a, b * a.L + t0 + t, d0 + c, x, dt, gy);
+        // channel k lies at k ^ (k >> 3): the vectors of 8 threads then meet all banks
 #pragma unroll
-        for (int s = 0; s < S; ++s) { h[e][s] = Gs[e][s] = 0.f; P[e][s] = 1.f; }
+        for (int j = 0; j < 8; ++j)
+            sd[t * CT + ((c + j) ^ (((c + j) >> 3) & 7))] = make_float4(dt[j], dt[j] * x[j], gy[j], 0.f);
+    }
+    stage_bc<IoT, T, Np, THREADS>(a, b, g, t0, nt, sB, sC);
+    f32x2 A2[S / 2], h[S / 2], Pr[S / 2], Gs[S / 2];
+    load_states<S>(a.A, d0 + ch, a.N, n0, ok, A2);
+    times_log2e<S>(A2);
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < S / 2; ++s) {
+        h[s] = Gs[s] = 0;
+        Pr[s] = f2_pack(1.f, 1.f);
+    }
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-        float B[S], C[S];
+    const float4* pd = sd + (ch ^ ((ch >> 3) & 7));
+#pragma unroll 4
+    for (int t = 0; t < T; ++t) {                        // tokens past the end have dt = 0 and g = 0
+        const float4 d = pd[t * CT];
+        f32x2 B[S / 2], C[S / 2];
+        f2_load<S>(sB + t * Np + n0, B);
+        f2_load<S>(sC + t * Np + n0, C);
+        const f32x2 dt = f2_pack(d.x, d.x), dx = f2_pack(d.y, d.y), gy = f2_pack(d.z, d.z);
+        sum += d.x;
 #pragma unroll
-        for (int s = 0; s < S; s += 4) {
-            Vec16<float>::load(sB + t * Np + n0 + s, B + s);
-            Vec16<float>::load(sC + t * Np + n0 + s, C + s);
-        }
-        const float2 dt2 = *(const float2*)(sdt + t * CT + ch), x2 = *(const float2*)(sx + t * CT + ch);
-        const float2 g2 = *(const float2*)(sg + t * CT + ch);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float dt = e ? dt2.y : dt2.x, dx = dt * (e ? x2.y : x2.x), gy = e ? g2.y : g2.x;
-            sum[e] += dt;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const float av = exp2_approx(dt * A2[e][s]);
-                h[e][s] = fmaf(av, h[e][s], dx * B[s]);
-                P[e][s] *= av;
-                Gs[e][s] = fmaf(P[e][s], C[s] * gy, Gs[e][s]);
-            }
+        for (int s = 0; s < S / 2; ++s) {
+            const f32x2 av = f2_exp2(f2_mul(dt, A2[s]));
+            h[s] = f2_fma(av, h[s], f2_mul(dx, B[s]));
+            Pr[s] = f2_mul(Pr[s], av);
+            Gs[s] = f2_fma(Pr[s], f2_mul(C[s], gy), Gs[s]);
         }
     }
-    float* wh = (float*)(a.ws + l.off_h);
-    float* wg = (float*)(a.ws + l.off_g);
-    const int64_t bc = b * l.nch + ck;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (!ok) continue;
-        if (n0 == 0) ((float*)(a.ws + l.off_dt))[bc * a.D + d0 + ch + e] = sum[e];
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (n0 + s < a.N) {
-                const int64_t k = (bc * a.D + d0 + ch + e) * a.N + n0 + s;
-                wh[k] = h[e][s];
-                wg[k] = Gs[e][s];
-            }
-    }
+    store_states<S>((float*)(a.ws + sh.off_h), bc * a.D + d0 + ch, a.N, n0, ok, h);
+    store_states<S>((float*)(a.ws + sh.off_g), bc * a.D + d0 + ch, a.N, n0, ok, Gs);
+    if (ok && n0 == 0) ((float*)(a.ws + sh.off_dt))[bc * a.D + d0 + ch] = sum;
 }
 
-// Thread = one state: the chunks' end states become the states that enter them,
-// their adjoints the ones that leave them.
+// Step 2, a thread a state: the first half of the blocks turns the chunks' end
+// states into the states that enter them, the second their adjoints into the
+// ones that leave them.  8 chunks' loads at a time.
 __global__ void __launch_bounds__(128)
-selective_bwd_chunks_kernel(const SelectiveArgs a, const SbLayout l) {
-    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, DN = a.D * a.N;
+selective_bwd_chunks_kernel(const SelectiveArgs a, const SbShape sh, int half) {
+    const bool back = (int)blockIdx.x >= half;
+    const int64_t i = (int64_t)(blockIdx.x - (back ? half : 0)) * 128 + threadIdx.x, DN = a.D * a.N;
     if (i >= a.batch * DN) return;
     const int64_t b = i / DN, dn = i % DN, d = dn / a.N;
     const float A2 = a.A[dn] * kLog2e;
-    float* wh = (float*)(a.ws + l.off_h) + b * l.nch * DN + dn;
-    float* wg = (float*)(a.ws + l.off_g) + b * l.nch * DN + dn;
-    const float* wdt = (const float*)(a.ws + l.off_dt) + b * l.nch * a.D + d;
-    float h = 0.f, w = 0.f;
-    if (a.init) h = a.state_bf16 ? to_f32(((const bf16*)a.init)[i]) : ((const float*)a.init)[i];
-    if (a.dfinal) w = a.state_bf16 ? to_f32(((const bf16*)a.dfinal)[i]) : ((const float*)a.dfinal)[i];
-    for (int64_t c = 0; c < l.nch; ++c) {
-        const float end = wh[c * DN];
-        wh[c * DN] = h;
-        h = fmaf(exp2_approx(wdt[c * a.D] * A2), h, end);
+    float* w = (float*)(a.ws + (back ? sh.off_g : sh.off_h)) + b * sh.nch * DN + dn;
+    const float* wdt = (const float*)(a.ws + sh.off_dt) + b * sh.nch * a.D + d;
+    const void* from = back ? a.dfinal : a.init;
+    float v = 0.f;
+    if (from) v = a.state_bf16 ? to_f32(((const bf16*)from)[i]) : ((const float*)from)[i];
+    const int64_t last = sh.nch - 1;
+    for (int64_t c0 = 0; c0 < sh.nch; c0 += 8) {
+        float own[8], dt[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int64_t c = back ? last - c0 - q : c0 + q;
+            own[q] = dt[q] = 0.f;
+            if (c0 + q < sh.nch) {
+                own[q] = w[c * DN];
+                dt[q] = wdt[c * a.D];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int64_t c = back ? last - c0 - q : c0 + q;
+            if (c0 + q >= sh.nch) break;
+            w[c * DN] = v;
+            v = fmaf(exp2_approx(dt[q] * A2), v, own[q]);
+        }
     }
-    for (int64_t c = l.nch - 1; c >= 0; --c) {
-        const float start = wg[c * DN];
-        wg[c * DN] = w;
-        w = fmaf(exp2_approx(wdt[c * a.D] * A2), w, start);
-    }
-    if (a.dinit) {
-        if (a.state_bf16) ((bf16*)a.dinit)[i] = from_f32<bf16>(w);
-        else ((float*)a.dinit)[i] = w;
+    if (back && a.dinit) {
+        if (a.state_bf16) ((bf16*)a.dinit)[i] = from_f32<bf16>(v);
+        else ((float*)a.dinit)[i] = v;
     }
 }
 
-template <typename IoT, typename GT, int S>
-__global__ void __launch_bounds__(kSbThreads)
-selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh, const SbLayout l) {
+// Sums v[i] over the P lanes (neighbours) that hold the same states of other
+// channels; the lane ends up with the sums of values first .. first + max(8 / P, 1).
+template <int P>
+__device__ __forceinline__ int sum_over_channels(float (&v)[8], int lane) {
+    int first = 0;
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+        if ((1 << step) >= P) break;
+        const int half = 4 >> step;
+        const bool up = lane & (1 << step);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= half) break;
+            const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 1 << step);
+        }
+        first += up ? half : 0;
+    }
+#pragma unroll
+    for (int o = 8; o < P; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    return first;
+}
+
+// Writes a round's values of the lane's states, [8 / S tokens][S] (S = 8: one
+// token), summed over the warp's channels, to the warp's rows of the chunk's sums.
+template <class Tile>
+__device__ __forceinline__ void put_sums(float (&v)[8], int lane, float* row) {
+    constexpr int P = Tile::P, S = Tile::S, Np = Tile::Np, LEFT = P >= 8 ? 1 : 8 / P;
+    const int first = sum_over_channels<P>(v, lane);
+    if (P > 8 && (lane & 8)) return;
+#pragma unroll
+    for (int i = 0; i < LEFT; ++i) {
+        const int k = first + i;
+        row[(k / S) * Np + k % S] = v[i];
+    }
+}
+
+// Step 3.
+template <typename IoT, typename GT_, class Tile>
+__global__ void __launch_bounds__(Tile::THREADS, 3)
+selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
+    constexpr int K = Tile::K, S = Tile::S, T = Tile::T, GT = Tile::GT, W = Tile::W, THREADS = Tile::THREADS;
+    constexpr int Np = Tile::Np, P = Tile::P, CT = Tile::CT, YS = Tile::YS, V = CT / 8, ACC = Tile::ACC;
+    constexpr int R = 8 / S;                                   // tokens of a round of sums over the channels
     extern __shared__ float4 smem4[];
-    const int T = l.T, CT = sh.CT, Np = sh.Np, K = sh.K;
-    float4* hs = smem4;                                // [T][2 S / 4][threads]
-    float* acc = (float*)(hs + T * (S / 2) * kSbThreads);   // [warps][T][dB, dC][Np]
-    float* sdt = acc + kSbWarps * T * 2 * Np;
-    float* sx = sdt + T * CT;
-    float* sg = sx + T * CT;
-    float* so = sg + T * CT;                           // [3][T][CT]: sum C h, sum G B, sum G A a h
-    float* sB = so + 3 * T * CT;
+    float4* sd = smem4;                                        // [T][CT / 2]: dt, dt, x, x; later dx, dx, d dt, d dt
+    float4* hs = sd + T * (CT / 2);                            // [T / GT - 1][2 S / 4][THREADS]
+    float2* sg = (float2*)(hs + (T / GT - 1) * (S / 2) * THREADS);   // [T][CT / 2]: g, g; later g x
+    float* sy = (float*)(sg + T * (CT / 2));                   // [T][YS]
+    float* sB = sy + T * YS;                                   // [T][Np]
     float* sC = sB + T * Np;
-    const int sp = (int)(blockIdx.x % (unsigned)l.split);
-    int64_t r = blockIdx.x / (unsigned)l.split;
+    float* acc = sC + T * Np;                                  // [W][T][Np]
+    const int sp = (int)(blockIdx.x % (unsigned)sh.split);
+    int64_t r = blockIdx.x / (unsigned)sh.split;
     const int64_t g = r % a.G;
     r /= a.G;
-    const int64_t ck = r % l.nch, b = r / l.nch, t0 = ck * l.T;
+    const int64_t ck = r % sh.nch, b = r / sh.nch, t0 = ck * T;
     const int nt = a.L - t0 < T ? (int)(a.L - t0) : T;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int pair = warp * (32 / K) + lane / K, n0 = (lane % K) * S, ch = pair * 2;
-    const int64_t bc = b * l.nch + ck, tok0 = b * a.L + t0;
-    for (int i = tid; i < kSbWarps * T * 2 * Np; i += kSbThreads) acc[i] = 0.f;
-    float* wacc = acc + warp * T * 2 * Np;
+    const int pair = warp * P + lane % P, n0 = (lane / P) * S, ch = pair * 2;
+    const int slot = pair ^ ((pair >> 3) & 7);                 // where the pair lies in a row of sd
+    const int64_t bc = b * sh.nch + ck, tok0 = b * a.L + t0;
+    const float* wh = (const float*)(a.ws + sh.off_h);
+    const float* wg = (const float*)(a.ws + sh.off_g);
+    float* wrow = acc + warp * T * Np + n0;
+    float accB[ACC], accC[ACC];
+#pragma unroll
+    for (int i = 0; i < ACC; ++i) accB[i] = accC[i] = 0.f;
+    stage_bc<IoT, T, Np, THREADS>(a, b, g, t0, nt, sB, sC);
 
-    for (int tile = sp; tile < sh.tiles; tile += l.split) {
+    for (int tile = sp; tile < sh.tiles; tile += sh.split) {
         const int c0 = tile * CT, nc = sh.Dg - c0 < CT ? sh.Dg - c0 : CT;
         const int64_t d0 = g * sh.Dg + c0;
         const bool ok = ch < nc;
-        __syncthreads();                               // the tile before has been read
-        sb_stage<IoT>(a, sh, T, b, g, t0, nt, d0, nc, sdt, sx, sg, tile == sp ? sB : nullptr, sC);
-        float A2[2][S], h[2][S], w[2][S], dA[2][S];
-        load_A<S>(a, d0 + ch, ok, n0, A2);
+        for (int i = tid; i < T * V; i += THREADS) {
+            const int t = i / V, c = (i % V) * 8;
+            float x[8], dt[8], gy[8];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+            for (int j = 0; j < 8; ++j) x[j] = dt[j] = gy[j] = 0.f;
+            if (t < nt && c < nc) load_token<IoT>(a, tok0 + t, d0 + c, x, dt, gy);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const bool in = ok && n0 + s < a.N;
-                const int64_t k = (bc * a.D + d0 + ch + e) * a.N + n0 + s;
-                h[e][s] = in ? ((const float*)(a.ws + l.off_h))[k] : 0.f;
-                w[e][s] = in ? ((const float*)(a.ws + l.off_g))[k] : 0.f;
-                dA[e][s] = 0.f;
+            for (int j = 0; j < 4; ++j) {
+                const int k = c / 2 + j;
+                sd[t * (CT / 2) + (k ^ ((k >> 3) & 7))] = make_float4(dt[2 * j], dt[2 * j + 1], x[2 * j], x[2 * j + 1]);
+                sg[t * (CT / 2) + k] = make_float2(gy[2 * j], gy[2 * j + 1]);
             }
-        __syncthreads();
-        for (int t = 0; t < nt; ++t) {
-            float B[S], C[S], y[2] = {0.f, 0.f}, dC[S];
-#pragma unroll
-            for (int s = 0; s < S; s += 4) {
-                Vec16<float>::load(sB + t * Np + n0 + s, B + s);
-                Vec16<float>::load(sC + t * Np + n0 + s, C + s);
-            }
-#pragma unroll
-            for (int s = 0; s < S; ++s) dC[s] = 0.f;
-            const float2 dt2 = *(const float2*)(sdt + t * CT + ch), x2 = *(const float2*)(sx + t * CT + ch);
-            const float2 g2 = *(const float2*)(sg + t * CT + ch);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float dt = e ? dt2.y : dt2.x, dx = dt * (e ? x2.y : x2.x), gy = e ? g2.y : g2.x;
-#pragma unroll
-                for (int s = 0; s < S; s += 4)
-                    hs[(t * (S / 2) + e * (S / 4) + s / 4) * kSbThreads + tid] =
-                        make_float4(h[e][s], h[e][s + 1], h[e][s + 2], h[e][s + 3]);
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    h[e][s] = fmaf(exp2_approx(dt * A2[e][s]), h[e][s], dx * B[s]);
-                    y[e] = fmaf(C[s], h[e][s], y[e]);
-                    dC[s] = fmaf(gy, h[e][s], dC[s]);
-                }
-            }
-            for (int o = 1; o < K; o <<= 1) {
-                y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
-                y[1] += __shfl_xor_sync(0xffffffffu, y[1], o);
-            }
-            if (n0 == 0) *(float2*)(so + t * CT + ch) = make_float2(y[0], y[1]);
-            for (int o = K; o < 32; o <<= 1)
-#pragma unroll
-                for (int s = 0; s < S; ++s) dC[s] += __shfl_xor_sync(0xffffffffu, dC[s], o);
-            if (lane < K)
-#pragma unroll
-                for (int s = 0; s < S; ++s) wacc[(t * 2 + 1) * Np + n0 + s] += dC[s];
         }
-        for (int t = nt - 1; t >= 0; --t) {
-            float B[S], C[S], wB[2] = {0.f, 0.f}, wA[2] = {0.f, 0.f}, dB[S];
+        f32x2 A2[2][S / 2], h[2][S / 2], w[2][S / 2], dA[2][S / 2];
 #pragma unroll
-            for (int s = 0; s < S; s += 4) {
-                Vec16<float>::load(sB + t * Np + n0 + s, B + s);
-                Vec16<float>::load(sC + t * Np + n0 + s, C + s);
+        for (int e = 0; e < 2; ++e) {
+            load_states<S>(a.A, d0 + ch + e, a.N, n0, ok, A2[e]);
+            times_log2e<S>(A2[e]);
+            load_states<S>(wh, bc * a.D + d0 + ch + e, a.N, n0, ok, h[e]);
+            load_states<S>(wg, bc * a.D + d0 + ch + e, a.N, n0, ok, w[e]);
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) dA[e][s] = 0;
+        }
+        const float Dv0 = ok && a.Dv ? a.Dv[d0 + ch] : 0.f, Dv1 = ok && a.Dv ? a.Dv[d0 + ch + 1] : 0.f;
+        __syncthreads();
+
+        // the states, every GT-th kept; y and dC
+        for (int tg = 0; tg < T / GT; ++tg) {
+            if (tg > 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int s = 0; s < S / 2; s += 2)
+                        ((ulonglong2*)hs)[((tg - 1) * (S / 2) + e * (S / 4) + s / 2) * THREADS + tid] =
+                            make_ulonglong2(h[e][s], h[e][s + 1]);
             }
 #pragma unroll
-            for (int s = 0; s < S; ++s) dB[s] = 0.f;
-            const float2 dt2 = *(const float2*)(sdt + t * CT + ch), x2 = *(const float2*)(sx + t * CT + ch);
-            const float2 g2 = *(const float2*)(sg + t * CT + ch);
+            for (int r0 = 0; r0 < GT; r0 += R < GT ? R : GT) {
+                float dC[8], y[2 * R];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float dt = e ? dt2.y : dt2.x, dx = dt * (e ? x2.y : x2.x), gy = e ? g2.y : g2.x;
+                for (int u = 0; u < R; ++u) {
+                    const int t = tg * GT + r0 + u;
+                    const float4 d = sd[t * (CT / 2) + slot];
+                    const float2 g2 = sg[t * (CT / 2) + pair];
+                    f32x2 B[S / 2], C[S / 2];
+                    f2_load<S>(sB + t * Np + n0, B);
+                    f2_load<S>(sC + t * Np + n0, C);
+                    f32x2 c[S / 2];
 #pragma unroll
-                for (int s4 = 0; s4 < S; s4 += 4) {
-                    const float4 hv = hs[(t * (S / 2) + e * (S / 4) + s4 / 4) * kSbThreads + tid];
-                    const float hp[4] = {hv.x, hv.y, hv.z, hv.w};
+                    for (int e = 0; e < 2; ++e) {
+                        const float dt1 = e ? d.y : d.x, dx1 = dt1 * (e ? d.w : d.z), g1 = e ? g2.y : g2.x;
+                        const f32x2 dt = f2_pack(dt1, dt1), dx = f2_pack(dx1, dx1), gy = f2_pack(g1, g1);
+                        f32x2 ys = 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int s = s4 + q;
-                        const float av = exp2_approx(dt * A2[e][s]);
-                        w[e][s] = fmaf(C[s], gy, w[e][s]);
-                        wB[e] = fmaf(w[e][s], B[s], wB[e]);
-                        dB[s] = fmaf(w[e][s], dx, dB[s]);
-                        w[e][s] *= av;                     // the adjoint one token back
-                        const float wah = w[e][s] * hp[q];
-                        wA[e] = fmaf(wah, A2[e][s], wA[e]);
-                        dA[e][s] = fmaf(wah, dt, dA[e][s]);
+                        for (int s = 0; s < S / 2; ++s) {
+                            h[e][s] = f2_fma(f2_exp2(f2_mul(dt, A2[e][s])), h[e][s], f2_mul(dx, B[s]));
+                            ys = s ? f2_fma(C[s], h[e][s], ys) : f2_mul(C[s], h[e][s]);
+                            c[s] = e ? f2_fma(gy, h[e][s], c[s]) : f2_mul(gy, h[e][s]);
+                        }
+                        const float2 yy = f2_get(ys);
+                        y[u * 2 + e] = yy.x + yy.y;
+                    }
+#pragma unroll
+                    for (int s = 0; s < S / 2; ++s) {
+                        const float2 v = f2_get(c[s]);
+                        dC[u * S + 2 * s] = v.x;
+                        dC[u * S + 2 * s + 1] = v.y;
+                    }
+                }
+                put_sums<Tile>(dC, lane, wrow + (tg * GT + r0) * Np);
+                if (a.z) {
+#pragma unroll
+                    for (int i = 0; i < 2 * R; ++i) {
+#pragma unroll
+                        for (int o = P; o < 32; o <<= 1) y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
+                    }
+                    if (n0 == 0) {
+#pragma unroll
+                        for (int u = 0; u < R; ++u)
+                            *(float2*)(sy + (tg * GT + r0 + u) * YS + ch) = make_float2(y[2 * u], y[2 * u + 1]);
                     }
                 }
             }
-            for (int o = 1; o < K; o <<= 1) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    wB[e] += __shfl_xor_sync(0xffffffffu, wB[e], o);
-                    wA[e] += __shfl_xor_sync(0xffffffffu, wA[e], o);
-                }
-            }
-            if (n0 == 0) {
-                *(float2*)(so + (T + t) * CT + ch) = make_float2(wB[0], wB[1]);
-                *(float2*)(so + (2 * T + t) * CT + ch) = make_float2(wA[0] * (1.f / kLog2e), wA[1] * (1.f / kLog2e));
-            }
-            for (int o = K; o < 32; o <<= 1)
-#pragma unroll
-                for (int s = 0; s < S; ++s) dB[s] += __shfl_xor_sync(0xffffffffu, dB[s], o);
-            if (lane < K)
-#pragma unroll
-                for (int s = 0; s < S; ++s) wacc[t * 2 * Np + n0 + s] += dB[s];
         }
-        float* wdA = (float*)(a.ws + l.off_dA);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (ok && n0 + s < a.N) wdA[(bc * a.D + d0 + ch + e) * a.N + n0 + s] = dA[e][s];
         __syncthreads();
-        // per channel and token: dx, d dt_raw, dz; d dt_raw and g x stay for their sums over the tokens
-        for (int i = tid; i < nt * (CT / 8); i += kSbThreads) {
-            const int t = i / (CT / 8), c = (i % (CT / 8)) * 8;
-            if (c >= nc) continue;
-            const int64_t at = (tok0 + t) * a.D + d0 + c;
-            float raw[8], dx[8], ddt[8];
-            load8((const IoT*)a.dt_raw + at, raw);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = t * CT + c + j;
-                const float wB = so[T * CT + k], Dv = a.Dv ? a.Dv[d0 + c + j] : 0.f;
-                dx[j] = fmaf(sdt[k], wB, Dv * sg[k]);
-                ddt[j] = fmaf(sx[k], wB, so[2 * T * CT + k]) * sigmoid_f32(raw[j] + (a.dt_bias ? a.dt_bias[d0 + c + j] : 0.f));
+        for (int i = 0; i < ACC; ++i) {
+            const int k = tid + i * THREADS;
+            if (k < T * Np) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) accC[i] += acc[q * T * Np + k];
             }
-            store8((GT*)a.dx + at, dx);
-            store8((GT*)a.ddt + at, ddt);
-            if (a.z) {
-                float z[8], dy[8], dz[8];
+        }
+        if (a.z) {
+            for (int i = tid; i < nt * V; i += THREADS) {
+                const int t = i / V, c = (i % V) * 8;
+                if (c >= nc) continue;
+                const int64_t at = (tok0 + t) * a.D + d0 + c;
+                float z[8], dy[8], x[8], dz[8], Dv[8];
                 load8((const IoT*)a.z + (tok0 + t) * a.zs + d0 + c, z);
                 load8((const IoT*)a.dy + at, dy);
+                load8((const IoT*)a.x + at, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) Dv[j] = 0.f;
+                if (a.Dv) load8(a.Dv + d0 + c, Dv);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int k = t * CT + c + j;
                     const float q = sigmoid_f32(z[j]);
-                    dz[j] = dy[j] * fmaf(a.Dv ? a.Dv[d0 + c + j] : 0.f, sx[k], so[k]) * q * fmaf(z[j], 1.f - q, 1.f);
+                    dz[j] = dy[j] * fmaf(Dv[j], x[j], sy[t * YS + c + j]) * q * fmaf(z[j], 1.f - q, 1.f);
                 }
-                store8((GT*)a.dz + at, dz);
+                store8((GT_*)a.dz + at, dz);
+            }
+        }
+        __syncthreads();                                       // acc is free again
+
+        // the adjoint back over the groups
+        for (int tg = T / GT - 1; tg >= 0; --tg) {
+            f32x2 av[GT][2][S / 2], hp[GT][2][S / 2];          // decay of token u, state before it
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (tg == 0) {
+                    load_states<S>(wh, bc * a.D + d0 + ch + e, a.N, n0, ok, hp[0][e]);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < S / 2; s += 2) {
+                        const ulonglong2 v = ((const ulonglong2*)hs)[((tg - 1) * (S / 2) + e * (S / 4) + s / 2) * THREADS + tid];
+                        hp[0][e][s] = v.x;
+                        hp[0][e][s + 1] = v.y;
+                    }
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = t * CT + c + j;
-                so[T * CT + k] = ddt[j];
-                so[k] = sg[k] * sx[k];
+            for (int u = 0; u < GT; ++u) {
+                const int t = tg * GT + u;
+                const float4 d = sd[t * (CT / 2) + slot];
+                f32x2 B[S / 2];
+                if (u + 1 < GT) f2_load<S>(sB + t * Np + n0, B);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float dt1 = e ? d.y : d.x, dx1 = dt1 * (e ? d.w : d.z);
+#pragma unroll
+                    for (int s = 0; s < S / 2; ++s) {
+                        av[u][e][s] = f2_exp2(f2_mul(f2_pack(dt1, dt1), A2[e][s]));
+                        if (u + 1 < GT)
+                            hp[u + 1][e][s] = f2_fma(av[u][e][s], hp[u][e][s], f2_mul(f2_pack(dx1, dx1), B[s]));
+                    }
+                }
             }
+            float vB[2 * GT], vA[2 * GT];                      // sums over the states, token u, channel e
+#pragma unroll
+            for (int r0 = GT - R; r0 >= 0; r0 -= R) {
+                float dB[8];
+#pragma unroll
+                for (int q = R - 1; q >= 0; --q) {
+                    const int u = r0 + q, t = tg * GT + u;
+                    const float4 d = sd[t * (CT / 2) + slot];
+                    const float2 g2 = sg[t * (CT / 2) + pair];
+                    f32x2 B[S / 2], C[S / 2], c[S / 2];
+                    f2_load<S>(sB + t * Np + n0, B);
+                    f2_load<S>(sC + t * Np + n0, C);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float dt1 = e ? d.y : d.x, dx1 = dt1 * (e ? d.w : d.z), g1 = e ? g2.y : g2.x;
+                        const f32x2 dt = f2_pack(dt1, dt1), dx = f2_pack(dx1, dx1), gy = f2_pack(g1, g1);
+                        f32x2 sb = 0, sa = 0;
+#pragma unroll
+                        for (int s = 0; s < S / 2; ++s) {
+                            w[e][s] = f2_fma(C[s], gy, w[e][s]);
+                            sb = s ? f2_fma(w[e][s], B[s], sb) : f2_mul(w[e][s], B[s]);
+                            c[s] = e ? f2_fma(w[e][s], dx, c[s]) : f2_mul(w[e][s], dx);
+                            w[e][s] = f2_mul(w[e][s], av[u][e][s]);         // the adjoint one token back
+                            const f32x2 wah = f2_mul(w[e][s], hp[u][e][s]);
+                            sa = s ? f2_fma(wah, A2[e][s], sa) : f2_mul(wah, A2[e][s]);
+                            dA[e][s] = f2_fma(wah, dt, dA[e][s]);
+                        }
+                        const float2 b2 = f2_get(sb), a2 = f2_get(sa);
+                        vB[u * 2 + e] = b2.x + b2.y;
+                        vA[u * 2 + e] = a2.x + a2.y;
+                    }
+#pragma unroll
+                    for (int s = 0; s < S / 2; ++s) {
+                        const float2 v = f2_get(c[s]);
+                        dB[q * S + 2 * s] = v.x;
+                        dB[q * S + 2 * s + 1] = v.y;
+                    }
+                }
+                put_sums<Tile>(dB, lane, wrow + (tg * GT + r0) * Np);
+            }
+            // dx and sum_n of d dt in the place of dt and x, whose last use this was
+            auto finish = [&](int u, float b0, float b1, float a0, float a1) {
+                const int t = tg * GT + u;
+                const float4 d = sd[t * (CT / 2) + slot];
+                const float2 g2 = sg[t * (CT / 2) + pair];
+                constexpr float ln2 = 0.6931471805599453f;     // A2 = A log2 e
+                sd[t * (CT / 2) + slot] = make_float4(fmaf(d.x, b0, Dv0 * g2.x), fmaf(d.y, b1, Dv1 * g2.y),
+                                                      fmaf(d.z, b0, a0 * ln2), fmaf(d.w, b1, a1 * ln2));
+                sg[t * (CT / 2) + pair] = make_float2(g2.x * d.z, g2.y * d.w);
+            };
+            if constexpr (GT == 4 && K <= 4) {
+                const int first = sum_over_states<K>(vB, lane);
+                sum_over_states<K>(vA, lane);
+                __syncwarp();                                  // the group's tokens have been read
+#pragma unroll
+                for (int i = 0; i < 4 / K; ++i) finish(first / 2 + i, vB[2 * i], vB[2 * i + 1], vA[2 * i], vA[2 * i + 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * GT; ++i) {
+#pragma unroll
+                    for (int o = P; o < 32; o <<= 1) {
+                        vB[i] += __shfl_xor_sync(0xffffffffu, vB[i], o);
+                        vA[i] += __shfl_xor_sync(0xffffffffu, vA[i], o);
+                    }
+                }
+                __syncwarp();
+                if (n0 == 0) {
+#pragma unroll
+                    for (int u = 0; u < GT; ++u) finish(u, vB[2 * u], vB[2 * u + 1], vA[2 * u], vA[2 * u + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            store_states<S>((float*)(a.ws + sh.off_dA), bc * a.D + d0 + ch + e, a.N, n0, ok, dA[e]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) {
+            const int k = tid + i * THREADS;
+            if (k < T * Np) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) accB[i] += acc[q * T * Np + k];
+            }
+        }
+        for (int i = tid; i < nt * V; i += THREADS) {
+            const int t = i / V, c = (i % V) * 8;
+            if (c >= nc) continue;
+            const int64_t at = (tok0 + t) * a.D + d0 + c;
+            float raw[8], bias[8], dx[8], ddt[8];
+            load8((const IoT*)a.dt_raw + at, raw);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+            if (a.dt_bias) load8(a.dt_bias + d0 + c, bias);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = c / 2 + j;
+                float4* p = sd + t * (CT / 2) + (k ^ ((k >> 3) & 7));
+                float4 v = *p;
+                v.z *= sigmoid_f32(raw[2 * j] + bias[2 * j]);
+                v.w *= sigmoid_f32(raw[2 * j + 1] + bias[2 * j + 1]);
+                dx[2 * j] = v.x;
+                dx[2 * j + 1] = v.y;
+                ddt[2 * j] = v.z;
+                ddt[2 * j + 1] = v.w;
+                *p = v;
+            }
+            store8((GT_*)a.dx + at, dx);
+            store8((GT_*)a.ddt + at, ddt);
         }
         __syncthreads();
-        for (int c = tid; c < nc; c += kSbThreads) {
-            float s0 = 0.f, s1 = 0.f;
-            for (int t = 0; t < nt; ++t) { s0 += so[(T + t) * CT + c]; s1 += so[t * CT + c]; }
-            float* par = (float*)(a.ws + l.off_par) + bc * 2 * a.D + d0 + c;
-            par[0] = s0;
-            par[a.D] = s1;
+        for (int i = tid; i < 2 * nc; i += THREADS) {          // sums over the chunk's tokens: d dt_raw, g x
+            const int which = i >= nc, c = which ? i - nc : i, k = c >> 1, e = c & 1;
+            const float* p = which ? (const float*)(sg + k) + e : (const float*)(sd + (k ^ ((k >> 3) & 7))) + 2 + e;
+            const int step = which ? CT : 2 * CT;
+            float s = 0.f;
+            for (int t = 0; t < nt; ++t) s += p[t * step];
+            ((float*)(a.ws + sh.off_par))[(bc * 2 + which) * a.D + d0 + c] = s;
         }
+        __syncthreads();                                       // the next tile is staged over these
     }
-    __syncthreads();
-    for (int i = tid; i < nt * 2 * Np; i += kSbThreads) {
-        const int n = i % Np, which = (i / Np) & 1, t = i / (2 * Np);
-        if (n >= a.N) continue;
-        float s = 0.f;
 #pragma unroll
-        for (int q = 0; q < kSbWarps; ++q) s += acc[q * T * 2 * Np + i];
-        float* out = (float*)(a.ws + (which ? l.off_dC : l.off_dB));
-        out[((int64_t)sp * a.batch * a.L + tok0 + t) * a.G * a.N + g * a.N + n] = s;
+    for (int i = 0; i < ACC; ++i) {
+        const int k = tid + i * THREADS, t = k / Np, n = k % Np;
+        if (k >= T * Np || t >= nt || n >= a.N) continue;
+        const int64_t at = ((int64_t)sp * a.batch * a.L + tok0 + t) * a.G * a.N + g * a.N + n;
+        ((float*)(a.ws + sh.off_dB))[at] = accB[i];
+        ((float*)(a.ws + sh.off_dC))[at] = accC[i];
     }
 }
 
@@ -439,43 +627,48 @@ __global__ void selective_bwd_empty_kernel(const SelectiveArgs a) {
     }
 }
 
-template <typename IoT, typename GT, int S>
+template <typename IoT, typename GT, class Sum, class Main>
 static cudaError_t launch_bwd_t(const SelectiveArgs& a, cudaStream_t s) {
-    const SbShape sh = sel_shape<S>(a.D, a.N, a.G, kSbWarps);
-    const SbLayout l = sb_layout(a.batch, a.L, a.D, a.N, a.G);
-    const int smem1 = (int)sizeof(float) * l.T * (3 * sh.CT + 2 * sh.Np);
-    const int smem3 = (int)sizeof(float) * l.T * (2 * S * kSbThreads + kSbWarps * 2 * sh.Np + 6 * sh.CT + 2 * sh.Np);
-    const auto k1 = selective_bwd_summary_kernel<IoT, S>;
-    const auto k3 = selective_bwd_main_kernel<IoT, GT, S>;
-    cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+    const SbShape sh = sb_shape(a.batch, a.L, a.D, a.N, a.G);
+    constexpr int smem1 = (int)sizeof(float) * Main::T * (4 * Sum::CT + 2 * Sum::Np), smem3 = Main::SMEM;
+    const auto k1 = selective_bwd_summary_kernel<IoT, Sum, Main::T>;
+    const auto k3 = selective_bwd_main_kernel<IoT, GT, Main>;
+    cudaError_t e = cudaSuccess;
+    if (smem1 > 48 * 1024) e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+    if (e == cudaSuccess && smem3 > 48 * 1024)
+        e = cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, smem3);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, smem3);
-    if (e != cudaSuccess) return e;
-    const int64_t chunks = a.batch * l.nch * a.G;
-    k1<<<(unsigned)(chunks * sh.tiles), kSbThreads, smem1, s>>>(a, sh, l);
-    selective_bwd_chunks_kernel<<<(unsigned)((a.batch * a.D * a.N + 127) / 128), 128, 0, s>>>(a, l);
-    k3<<<(unsigned)(chunks * l.split), kSbThreads, smem3, s>>>(a, sh, l);
+    const int64_t chunks = a.batch * sh.nch * a.G;
+    const int half = (int)((a.batch * a.D * a.N + 127) / 128);
+    k1<<<(unsigned)(chunks * sh.tiles1), Sum::W * 32, smem1, s>>>(a, sh);
+    selective_bwd_chunks_kernel<<<(unsigned)(2 * half), 128, 0, s>>>(a, sh, half);
+    k3<<<(unsigned)(chunks * sh.split), Main::THREADS, smem3, s>>>(a, sh);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t bn = a.batch * l.nch, DN = a.D * a.N, M = a.batch * a.L * a.G * a.N;
+    const int64_t bn = a.batch * sh.nch, DN = a.D * a.N, M = a.batch * a.L * a.G * a.N;
     const bool gb = sizeof(GT) == 2;
-    const float* par = (const float*)(a.ws + l.off_par);
-    e = launch_column_sum((const float*)(a.ws + l.off_dA), bn, DN, DN, a.dA, false, s);
+    const float* par = (const float*)(a.ws + sh.off_par);
+    e = launch_column_sum((const float*)(a.ws + sh.off_dA), bn, DN, DN, a.dA, false, s);
     if (e == cudaSuccess && a.ddt_bias) e = launch_column_sum(par, bn, 2 * a.D, a.D, a.ddt_bias, false, s);
     if (e == cudaSuccess && a.dD) e = launch_column_sum(par + a.D, bn, 2 * a.D, a.D, a.dD, false, s);
-    if (e == cudaSuccess) e = launch_column_sum((const float*)(a.ws + l.off_dB), l.split, M, M, a.dB, gb, s);
-    if (e == cudaSuccess) e = launch_column_sum((const float*)(a.ws + l.off_dC), l.split, M, M, a.dC, gb, s);
+    if (e == cudaSuccess) e = launch_column_sum((const float*)(a.ws + sh.off_dB), sh.split, M, M, a.dB, gb, s);
+    if (e == cudaSuccess) e = launch_column_sum((const float*)(a.ws + sh.off_dC), sh.split, M, M, a.dC, gb, s);
     return e;
 }
 
 template <typename IoT, typename GT>
 static cudaError_t launch_bwd_s(const SelectiveArgs& a, cudaStream_t s) {
-    return sb_states(a.N) == 8 ? launch_bwd_t<IoT, GT, 8>(a, s) : launch_bwd_t<IoT, GT, 4>(a, s);
+    if (a.N <= 8) return launch_bwd_t<IoT, GT, SelTile<2, 4, 8>, SbTile<2, 4, 16, 4>>(a, s);
+    if (a.N <= 16) return launch_bwd_t<IoT, GT, SelTile<4, 4, 8>, SbTile<4, 4, 32, 4>>(a, s);
+    if (a.N <= 32) return launch_bwd_t<IoT, GT, SelTile<8, 4, 8>, SbTile<8, 4, 32, 4>>(a, s);
+    if (a.N <= 64) return launch_bwd_t<IoT, GT, SelTile<16, 4, 8>, SbTile<16, 4, 16, 4>>(a, s);
+    if (a.N <= 128) return launch_bwd_t<IoT, GT, SelTile<32, 4, 16>, SbTile<32, 4, 16, 4>>(a, s);
+    return launch_bwd_t<IoT, GT, SelTile<32, 8, 8>, SbTile<32, 8, 8, 2>>(a, s);
 }
 
 cudaError_t launch_selective_bwd(const SelectiveArgs& a, cudaStream_t s) {
     if (a.batch == 0 || a.L == 0) {
-        int64_t n = a.D * a.N * (a.batch > 1 ? a.batch : 1);
+        const int64_t n = a.D * a.N * (a.batch > 1 ? a.batch : 1);
         selective_bwd_empty_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
         return cudaGetLastError();
     }
