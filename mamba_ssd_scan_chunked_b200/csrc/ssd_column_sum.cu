@@ -11,7 +11,8 @@ namespace ssd {
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t stride, int64_t cols, T* __restrict__ out) {
+column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t stride, int64_t cols, T* __restrict__ out,
+                  int64_t cols1, T* __restrict__ out2) {
     __shared__ float sums[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
@@ -25,7 +26,8 @@ column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t stride, 
     if (warp == 0 && c < cols) {
 #pragma unroll
         for (int w = 1; w < 8; ++w) s += sums[w][lane];
-        out[c] = from_f32<T>(s);
+        if (c < cols1) out[c] = from_f32<T>(s);
+        else if (out2) out2[c - cols1] = from_f32<T>(s);
     }
 }
 
@@ -33,8 +35,15 @@ cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t stride, i
                               cudaStream_t s) {
     if (cols == 0) return cudaSuccess;
     const unsigned grid = (unsigned)((cols + 31) / 32);
-    if (out_bf16) column_sum_kernel<bf16><<<grid, 256, 0, s>>>(part, rows, stride, cols, (bf16*)out);
-    else column_sum_kernel<float><<<grid, 256, 0, s>>>(part, rows, stride, cols, (float*)out);
+    if (out_bf16) column_sum_kernel<bf16><<<grid, 256, 0, s>>>(part, rows, stride, cols, (bf16*)out, cols, nullptr);
+    else column_sum_kernel<float><<<grid, 256, 0, s>>>(part, rows, stride, cols, (float*)out, cols, nullptr);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_column_sum2(const float* part, int64_t rows, int64_t cols, float* out, int64_t cols1, float* out2,
+                               cudaStream_t s) {
+    if (cols == 0) return cudaSuccess;
+    column_sum_kernel<float><<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(part, rows, cols, cols, out, cols1, out2);
     return cudaGetLastError();
 }
 

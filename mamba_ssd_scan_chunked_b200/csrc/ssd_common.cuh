@@ -88,29 +88,4 @@ template <> struct Vec16<bf16> {
     }
 };
 
-// 8 consecutive elements (16-byte aligned) to and from fp32.
-__device__ __forceinline__ void load8(const bf16* p, float* v) { Vec16<bf16>::load(p, v); }
-__device__ __forceinline__ void load8(const float* p, float* v) {
-    Vec16<float>::load(p, v);
-    Vec16<float>::load(p + 4, v + 4);
-}
-__device__ __forceinline__ void store8(bf16* p, const float* v) { Vec16<bf16>::store(p, v); }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-    Vec16<float>::store(p, v);
-    Vec16<float>::store(p + 4, v + 4);
-}
-// the same of an array whose dtype is known at run time only
-__device__ __forceinline__ void load8_dyn(const void* p, bool is_bf16, int64_t i, float* v) {
-    if (is_bf16) load8((const bf16*)p + i, v);
-    else load8((const float*)p + i, v);
-}
-__device__ __forceinline__ void store8_dyn(void* p, bool is_bf16, int64_t i, const float* v) {
-    if (is_bf16) store8((bf16*)p + i, v);
-    else store8((float*)p + i, v);
-}
-
-// 1 / (1 + e^-v).  e^-v overflows to infinity below v = -88, where the result
-// is 0 in fp32; the quotient's approximation is within 2 units in the last place.
-__device__ __forceinline__ float sigmoid_f32(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-
 }  // namespace ssd

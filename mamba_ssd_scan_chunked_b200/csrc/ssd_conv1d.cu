@@ -7,8 +7,10 @@
 // Every kernel is a stream bound by HBM: a thread owns a few neighbouring
 // channels, walks over a run of tokens with the last W - 1 inputs in registers,
 // and so reads each input once (and W - 1 more per run).
-#include "ssd_common.cuh"
+#include <type_traits>
+
 #include "ssd_internal.h"
+#include "ssd_vec.cuh"
 
 namespace ssd {
 
@@ -89,54 +91,113 @@ __device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int6
     }
 }
 
-constexpr int kFwdThreads = 128, kFwdTokens = 16;
+// VEC channels of a token as they lie in memory (8 or 16 bytes, all loads of a
+// round in flight before the first is used)
+template <typename T, int VEC> struct RawVec {
+    typename std::conditional<sizeof(T) * VEC == 16, uint4, uint2>::type r;
+    __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const decltype(r)*>(p); }
+    __device__ __forceinline__ void get(f32x2 (&v)[VEC / 2]) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            if constexpr (sizeof(T) == 2) v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            else v[i] = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        }
+    }
+};
+
+template <int N, int VEC>
+__device__ __forceinline__ void pairs(const float (&v)[N][VEC], f32x2 (&out)[N][VEC / 2]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) out[k][i] = f2_pack(v[k][2 * i], v[k][2 * i + 1]);
+}
+
+// The forward: kFwdRound tokens' loads are in flight while the round before is
+// computed.  A run of 32 tokens reads 3 / 32 of its inputs twice and its filter
+// once per 512 bytes of input; where there are fewer threads than keep an SM's
+// loads in flight, runs of 8.
+constexpr int kFwdThreads = 128, kFwdRound = 4;
 
 template <typename IoT, typename YT, int W>
 __global__ void __launch_bounds__(kFwdThreads)
-conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
-    constexpr int VEC = 16 / sizeof(IoT);
+conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
+    constexpr int VEC = 16 / sizeof(IoT), H = VEC / 2, U = kFwdRound;
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * kFwdThreads + threadIdx.x) * VEC;
     const int64_t bs = blockIdx.x / (unsigned)cblocks;
     const int64_t b = bs / nseg, seg = bs % nseg;
     if (c >= a.D) return;
     int64_t p = a.pad_left ? a.pad_left[b] : 0;
     p = p < 0 ? 0 : p > a.L ? a.L : p;
-    const int64_t t0 = seg * kFwdTokens;
-    const int64_t t1 = t0 + kFwdTokens < a.L ? t0 + kFwdTokens : a.L;
-
-    float w[W][VEC], bias[VEC], win[W][VEC];
-    load_taps<W, VEC>(a.w, c, w);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
-    load_window<IoT, W, VEC>(a, b, c, t0, p, win);
+    const int64_t t0 = seg * run;
+    const int64_t t1 = t0 + run < a.L ? t0 + run : a.L;
     int64_t ld, at;
     const int which = split_of(a, c, &ld, &at);
-    YT* y = (YT*)a.y[which] + (b * a.L) * ld + at;
-    for (int64_t t = t0; t < t1; ++t) {
-        float out[VEC];
-        if (t >= p) {
-            loadv<VEC>((const IoT*)a.x + (b * a.L + t) * a.xs + c, win[W - 1]);
+    YT* y = (YT*)a.y[which] + (b * a.L + t0) * ld + at;
+    const IoT* x = (const IoT*)a.x + (b * a.L + t0) * a.xs + c;
+    const int len = (int)(t1 - t0), lead = t0 < p ? (int)((p < t1 ? p : t1) - t0) : 0;   // lead: absent tokens
+
+    RawVec<IoT, VEC> next[U];
+    auto load = [&](int t) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float v = bias[i];
+        for (int u = 0; u < U; ++u)
+            if (t + u >= lead && t + u < len) next[u].load(x + (t + u) * a.xs);
+    };
+    load(0);
+    f32x2 w[W][H], win[W][H], bias[H];
+    {
+        float wf[W][VEC], winf[W][VEC] = {};
+        load_taps<W, VEC>(a.w, c, wf);
+        pairs<W, VEC>(wf, w);
+        load_window<IoT, W, VEC>(a, b, c, t0, p, winf);
+        pairs<W, VEC>(winf, win);
 #pragma unroll
-                for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[k][i], v);
-                out[i] = a.silu ? v * sigmoid_f32(v) : v;
+        for (int i = 0; i < H; ++i) bias[i] = a.bias ? f2_pack(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
+    }
+    for (int t = 0; t < len; t += U) {
+        RawVec<IoT, VEC> now[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+        load(t + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u >= len) break;
+            float out[VEC];
+            if (t + u >= lead) {
+                now[u].get(win[W - 1]);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    f32x2 v = bias[i];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], win[k][i], v);
+                    const float2 r = f2_get(v);
+                    out[2 * i] = a.silu ? r.x * sigmoid_f32(r.x) : r.x;
+                    out[2 * i + 1] = a.silu ? r.y * sigmoid_f32(r.y) : r.y;
+                }
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) win[k][i] = win[k + 1][i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) out[i] = 0.f;
             }
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) win[k][i] = win[k + 1][i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) out[i] = 0.f;
+            storev<VEC>(y + (t + u) * ld, out);
         }
-        storev<VEC>(y + t * ld, out);
     }
     if (a.final_state && seg == nseg - 1) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            store_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, win[j]);
+        for (int j = 0; j < W - 1; ++j) {
+            float f[VEC];
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 r = f2_get(win[j][i]);
+                f[2 * i] = r.x;
+                f[2 * i + 1] = r.y;
+            }
+            store_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, f);
+        }
     }
 }
 
@@ -172,94 +233,134 @@ conv1d_update_kernel(const Conv1dArgs a, int cblocks) {
 
 // Backward.  A block is 32 lanes (4 channels each) x 8 warps; warp q walks over
 // the kBwdTokens tokens of its run and the W - 1 after it (whose dv its last dx
-// need).  dx of a token is complete W - 1 tokens later.  The block's sums of dw
-// and db go to one row of the partial sums.
-constexpr int kBwdWarps = 8, kBwdTokens = 16, kBwdVec = 4;
+// need), loads a round ahead.  dx of a token is complete W - 1 tokens later.  The
+// block's sums of dw and db go to one row of the partial sums.
+constexpr int kBwdWarps = 8, kBwdTokens = 32, kBwdVec = 4, kBwdRound = 4;
 
 template <typename IoT, typename GT, int W>
 __global__ void __launch_bounds__(kBwdWarps * 32)
 conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
-    constexpr int VEC = kBwdVec;
+    constexpr int VEC = kBwdVec, H = VEC / 2, U = kBwdRound;
     __shared__ float sums[kBwdWarps][(W + 1) * VEC][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * 32 + lane) * VEC;
     const int64_t bs = blockIdx.x / (unsigned)cblocks;
     const int64_t b = bs / nseg, seg = bs % nseg;
     const int64_t t0 = (seg * kBwdWarps + warp) * kBwdTokens;
-    const int64_t t1 = t0 + kBwdTokens < a.L ? t0 + kBwdTokens : a.L;
-    float dw[W][VEC], db[VEC];
+    f32x2 dw[W][H], db[H];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < H; ++i) {
+        db[i] = 0;
 #pragma unroll
-        for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
+        for (int k = 0; k < W; ++k) dw[k][i] = 0;
     }
     if (c < a.D && (t0 < a.L || t0 == 0)) {
-        float w[W][VEC], bias[VEC], win[W][VEC], pend[W][VEC];
-        load_taps<W, VEC>(a.w, c, w);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
-        load_window<IoT, W, VEC>(a, b, c, t0, 0, win);
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) pend[k][i] = 0.f;
         int64_t ld, at;
         const int which = split_of(a, c, &ld, &at);
-        const IoT* dy = (const IoT*)a.dy[which] + (b * a.L) * ld + at;
-        for (int64_t t = t0; t < t1 + W - 1; ++t) {
-            if (t < a.L) {
-                float dv[VEC];
-                loadv<VEC>((const IoT*)a.x + (b * a.L + t) * a.xs + c, win[W - 1]);
-                loadv<VEC>(dy + t * ld, dv);
-                const bool mine = t < t1;
+        const IoT* dy = (const IoT*)a.dy[which] + (b * a.L + t0) * ld + at;
+        const IoT* x = (const IoT*)a.x + (b * a.L + t0) * a.xs + c;
+        GT* dx = (GT*)a.dx + (b * a.L + t0) * a.dxs + c;
+        const int left = a.L - t0 < (1 << 20) ? (int)(a.L - t0) : 1 << 20;   // tokens from t0 on
+        const int len = left < kBwdTokens ? left : kBwdTokens;
+        RawVec<IoT, VEC> nx[U], ny[U];
+        auto load = [&](int t) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    if (a.silu) {
-                        float v = bias[i];
+            for (int u = 0; u < U; ++u)
+                if (t + u < left && t + u < len + W - 1) {
+                    nx[u].load(x + (t + u) * a.xs);
+                    ny[u].load(dy + (t + u) * ld);
+                }
+        };
+        load(0);
+        f32x2 w[W][H], win[W][H], pend[W][H], bias[H];
+        {
+            float wf[W][VEC], winf[W][VEC] = {};
+            load_taps<W, VEC>(a.w, c, wf);
+            pairs<W, VEC>(wf, w);
+            load_window<IoT, W, VEC>(a, b, c, t0, 0, winf);
+            pairs<W, VEC>(winf, win);
 #pragma unroll
-                        for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[k][i], v);
-                        const float g = sigmoid_f32(v);
-                        dv[i] *= g * fmaf(v, 1.f - g, 1.f);
+            for (int i = 0; i < H; ++i) bias[i] = a.bias ? f2_pack(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+#pragma unroll
+                for (int i = 0; i < H; ++i) pend[k][i] = 0;
+        }
+        for (int t = 0; t < len + W - 1; t += U) {
+            RawVec<IoT, VEC> now[U], dyn[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                now[u] = nx[u];
+                dyn[u] = ny[u];
+            }
+            load(t + U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= len + W - 1) break;
+                if (t + u < left) {
+                    f32x2 dv[H];
+                    now[u].get(win[W - 1]);
+                    dyn[u].get(dv);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        if (a.silu) {
+                            f32x2 v = bias[i];
+#pragma unroll
+                            for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], win[k][i], v);
+                            const float2 r = f2_get(v);
+                            dv[i] = f2_mul(dv[i], f2_pack(silu_grad(r.x, sigmoid_f32(r.x)), silu_grad(r.y, sigmoid_f32(r.y))));
+                        }
+                        if (t + u < len) {
+                            db[i] = f2_fma(dv[i], f2_pack(1.f, 1.f), db[i]);
+#pragma unroll
+                            for (int k = 0; k < W; ++k) dw[k][i] = f2_fma(dv[i], win[k][i], dw[k][i]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < W; ++k) pend[k][i] = f2_fma(w[k][i], dv[i], pend[k][i]);
                     }
-                    if (mine) {
-                        db[i] += dv[i];
 #pragma unroll
-                        for (int k = 0; k < W; ++k) dw[k][i] = fmaf(dv[i], win[k][i], dw[k][i]);
+                    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                        for (int i = 0; i < H; ++i) win[k][i] = win[k + 1][i];
+                }
+                const int s = t + u - (W - 1);        // the input (from t0 on) whose gradient is now complete
+                if (s >= 0 || t0 == 0) {
+                    float g[VEC];
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float2 r = f2_get(pend[0][i]);
+                        g[2 * i] = r.x;
+                        g[2 * i + 1] = r.y;
                     }
+                    if (a.dfinal && s >= left - (W - 1)) {
+                        float f[VEC];
+                        load_state<VEC>(a.dfinal, a.state_bf16, (b * (W - 1) + s - left + W - 1) * a.D + c, f);
 #pragma unroll
-                    for (int k = 0; k < W; ++k) pend[k][i] = fmaf(w[k][i], dv[i], pend[k][i]);
+                        for (int i = 0; i < VEC; ++i) g[i] += f[i];
+                    }
+                    if (s >= 0) storev<VEC>(dx + s * a.dxs, g);
+                    else if (a.dinit) store_state<VEC>(a.dinit, a.state_bf16, (b * (W - 1) + s + W - 1) * a.D + c, g);
                 }
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k)
+                for (int i = 0; i < H; ++i) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) win[k][i] = win[k + 1][i];
-            }
-            const int64_t s = t - (W - 1);            // the input whose gradient is now complete
-            if (s >= t0 || t0 == 0) {
-                if (a.dfinal && s >= a.L - (W - 1)) {
-                    float f[VEC];
-                    load_state<VEC>(a.dfinal, a.state_bf16, (b * (W - 1) + s - a.L + W - 1) * a.D + c, f);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) pend[0][i] += f[i];
+                    for (int k = 0; k < W - 1; ++k) pend[k][i] = pend[k + 1][i];
+                    pend[W - 1][i] = 0;
                 }
-                if (s >= 0) storev<VEC>((GT*)a.dx + (b * a.L + s) * a.dxs + c, pend[0]);
-                else if (a.dinit)
-                    store_state<VEC>(a.dinit, a.state_bf16, (b * (W - 1) + s + W - 1) * a.D + c, pend[0]);
             }
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) pend[k][i] = pend[k + 1][i];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) pend[W - 1][i] = 0.f;
         }
     }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int i = 0; i < H; ++i) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) sums[warp][i * W + k][lane] = dw[k][i];
-        sums[warp][W * VEC + i][lane] = db[i];
+        for (int k = 0; k < W; ++k) {
+            const float2 r = f2_get(dw[k][i]);
+            sums[warp][2 * i * W + k][lane] = r.x;
+            sums[warp][(2 * i + 1) * W + k][lane] = r.y;
+        }
+        const float2 r = f2_get(db[i]);
+        sums[warp][W * VEC + 2 * i][lane] = r.x;
+        sums[warp][W * VEC + 2 * i + 1][lane] = r.y;
     }
     __syncthreads();
     float* row = a.ws + bs * (a.D * (W + 1));
@@ -279,7 +380,10 @@ __global__ void conv1d_zero_kernel(float* dw, float* db, int64_t nw, int64_t nb)
     }
 }
 
-static int64_t fwd_segments(int64_t L) { return L > 0 ? (L + kFwdTokens - 1) / kFwdTokens : 1; }
+// tokens a thread walks over: 32 from 512 threads an SM on
+static int fwd_run(int64_t batch, int64_t L, int64_t vecs) { return batch * ((L + 31) / 32) * vecs >= 148 * 512 ? 32 : 8; }
+
+static int64_t fwd_segments(int64_t L, int run) { return L > 0 ? (L + run - 1) / run : 1; }
 
 static int64_t bwd_segments(int64_t L) {
     const int64_t run = kBwdWarps * kBwdTokens;
@@ -289,7 +393,7 @@ static int64_t bwd_segments(int64_t L) {
 int64_t conv1d_bwd_segments(int64_t batch, int64_t L) { return batch * bwd_segments(L); }
 
 int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D) {
-    return batch * fwd_segments(L) * ((D / 4 + 31) / 32);
+    return batch * fwd_segments(L, 8) * ((D / 4 + 31) / 32);
 }
 
 // calls f<IoT, OutT, W>() for the types and taps of a
@@ -306,9 +410,10 @@ int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D) {
 
 cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s) {
     const int vec = a.io_bf16 ? 8 : 4;
-    const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads), nseg = (int)fwd_segments(a.L);
+    const int run = fwd_run(a.batch, a.L, a.D / vec);
+    const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads), nseg = (int)fwd_segments(a.L, run);
     const unsigned grid = (unsigned)(a.batch * nseg * cblocks);
-#define FN(IO, Y, W_) conv1d_fwd_kernel<IO, Y, W_><<<grid, kFwdThreads, 0, s>>>(a, cblocks, nseg)
+#define FN(IO, Y, W_) conv1d_fwd_kernel<IO, Y, W_><<<grid, kFwdThreads, 0, s>>>(a, cblocks, nseg, run)
     CONV1D_DISPATCH(FN);
 #undef FN
     return cudaGetLastError();
@@ -335,11 +440,9 @@ cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s) {
 #define FN(IO, G_, W_) conv1d_bwd_kernel<IO, G_, W_><<<grid, kBwdWarps * 32, 0, s>>>(a, cblocks, nseg)
     CONV1D_DISPATCH(FN);
 #undef FN
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_column_sum(a.ws, a.batch * nseg, nw + a.D, nw, a.dw, false, s);
-    if (e != cudaSuccess || !a.db) return e;
-    return launch_column_sum(a.ws + nw, a.batch * nseg, nw + a.D, a.D, a.db, false, s);
+    return launch_column_sum2(a.ws, a.batch * nseg, nw + a.D, a.dw, nw, a.db, s);
 }
 
 }  // namespace ssd

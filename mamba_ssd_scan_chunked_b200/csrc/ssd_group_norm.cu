@@ -13,8 +13,8 @@
 // go to slots: `lanes` neighbouring threads each, up to a warp, or the whole
 // block.  The number of slots is a multiple of the groups, so that a slot meets
 // one group only and keeps its weights, and the sums of dw and db, in registers.
-#include "ssd_common.cuh"
 #include "ssd_internal.h"
+#include "ssd_vec.cuh"
 
 namespace ssd {
 
@@ -134,11 +134,6 @@ group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
     }
 }
 
-__device__ __forceinline__ float silu_grad(float v) {
-    const float g = sigmoid_f32(v);
-    return g * fmaf(v, 1.f - g, 1.f);
-}
-
 template <typename XT, typename IoT, typename GT, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 1024 : 128)
 group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
@@ -177,9 +172,9 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 float dv = dn[q][j];
                 const float v = fmaf(t.u[q][j], w[j], bias[j]);
                 if (a.act == kSilu) {
-                    dv *= silu_grad(v);
+                    dv *= silu_grad(v, sigmoid_f32(v));
                 } else if (a.act == kAfter) {
-                    dz[j] = dv * v * silu_grad(z[q][j]);
+                    dz[j] = dv * v * silu_grad(z[q][j], sigmoid_f32(z[q][j]));
                     dv *= z[q][j] * sigmoid_f32(z[q][j]);
                 }
                 dw[q][j] = fmaf(dv, t.u[q][j], dw[q][j]);
@@ -202,7 +197,7 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 dx[j] = du;
                 if (a.act == kBefore) {
                     dx[j] = du * (z[q][j] * sigmoid_f32(z[q][j]));
-                    dz[j] = du * x[q][j] * silu_grad(z[q][j]);
+                    dz[j] = du * x[q][j] * silu_grad(z[q][j], sigmoid_f32(z[q][j]));
                 }
             }
             if (live && i < sh.gs) {

@@ -274,6 +274,9 @@ cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s);
 // (ssd_column_sum.cu); out is bf16 or fp32
 cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t stride, int64_t cols, void* out, bool out_bf16,
                               cudaStream_t s);
+// the same into two arrays: columns 0 .. cols1 - 1 to out, the others to out2 (not written when NULL)
+cudaError_t launch_column_sum2(const float* part, int64_t rows, int64_t cols, float* out, int64_t cols1, float* out2,
+                               cudaStream_t s);
 
 // fault-injection bits set by ssd_debug_inject (read at every launch)
 uint32_t debug_faults();

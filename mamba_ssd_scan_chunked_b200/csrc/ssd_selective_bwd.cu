@@ -443,7 +443,7 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float q = sigmoid_f32(z[j]);
-                    dz[j] = dy[j] * fmaf(Dv[j], x[j], sy[t * YS + c + j]) * q * fmaf(z[j], 1.f - q, 1.f);
+                    dz[j] = dy[j] * fmaf(Dv[j], x[j], sy[t * YS + c + j]) * silu_grad(z[j], q);
                 }
                 store8((GT_*)a.dz + at, dz);
             }

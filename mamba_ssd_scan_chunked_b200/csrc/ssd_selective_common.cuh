@@ -5,42 +5,11 @@
 // state at 0), and a warp covers 32 / K pairs of channels.
 #pragma once
 
-#include "ssd_common.cuh"
 #include "ssd_internal.h"
+#include "ssd_vec.cuh"
 
 namespace ssd {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_approx(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// Two fp32 operations in one instruction (neighbouring states of a lane): the
-// rate of the arithmetic is the same, the issue slots are halved.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 f2_pack(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 f2_get(f32x2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ f32x2 f2_exp2(f32x2 v) {
     const float2 t = f2_get(v);
     return f2_pack(exp2_approx(t.x), exp2_approx(t.y));
@@ -80,31 +49,6 @@ __device__ __forceinline__ f32x2 softplus2(float z0, float z1) {
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m1) : "f"(z1));
     return f2_fma(p, e, f2_pack(m0, m1));
 }
-
-// 8 elements as they lie in memory, widened when they are used
-template <typename T> struct Raw8;
-template <> struct Raw8<bf16> {
-    uint4 r;
-    __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void minus_inf() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
-    __device__ __forceinline__ void get(float* v) const { Vec16<bf16>::unpack(r, v); }
-};
-template <> struct Raw8<float> {
-    uint4 r[2];
-    __device__ __forceinline__ void load(const float* p) {
-        r[0] = *reinterpret_cast<const uint4*>(p);
-        r[1] = *reinterpret_cast<const uint4*>(p + 4);
-    }
-    __device__ __forceinline__ void zero() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void minus_inf() {
-        r[0] = r[1] = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-    }
-    __device__ __forceinline__ void get(float* v) const {
-        Vec16<float>::unpack(r[0], v);
-        Vec16<float>::unpack(r[1], v + 4);
-    }
-};
 
 // Lanes and channels: a lane holds S neighbouring states of one channel, K lanes
 // (a power of two) its N states, padded with A = B = C = 0, which keep a state at

@@ -1,0 +1,98 @@
+// Device-side helpers of the operators around the scan: vectors of 8 elements,
+// approximations of the special functions, pairs of fp32 operations.
+#pragma once
+
+#include "ssd_common.cuh"
+
+namespace ssd {
+
+// 8 consecutive elements (16-byte aligned) to and from fp32.
+__device__ __forceinline__ void load8(const bf16* p, float* v) { Vec16<bf16>::load(p, v); }
+__device__ __forceinline__ void load8(const float* p, float* v) {
+    Vec16<float>::load(p, v);
+    Vec16<float>::load(p + 4, v + 4);
+}
+__device__ __forceinline__ void store8(bf16* p, const float* v) { Vec16<bf16>::store(p, v); }
+__device__ __forceinline__ void store8(float* p, const float* v) {
+    Vec16<float>::store(p, v);
+    Vec16<float>::store(p + 4, v + 4);
+}
+// the same of an array whose dtype is known at run time only
+__device__ __forceinline__ void load8_dyn(const void* p, bool is_bf16, int64_t i, float* v) {
+    if (is_bf16) load8((const bf16*)p + i, v);
+    else load8((const float*)p + i, v);
+}
+__device__ __forceinline__ void store8_dyn(void* p, bool is_bf16, int64_t i, const float* v) {
+    if (is_bf16) store8((bf16*)p + i, v);
+    else store8((float*)p + i, v);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / (1 + e^-v).  e^-v overflows to infinity below v = -88, where the result
+// is 0 in fp32; the two approximations are within 2 units in the last place each.
+__device__ __forceinline__ float sigmoid_f32(float v) { return rcp_approx(1.f + exp2_approx(-kLog2e * v)); }
+// d silu(v) / dv from g = sigmoid(v)
+__device__ __forceinline__ float silu_grad(float v, float g) { return g * fmaf(v, 1.f - g, 1.f); }
+
+// Two fp32 operations in one instruction (neighbouring states or channels of a lane): the
+// rate of the arithmetic is the same, the issue slots are halved.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 f2_pack(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// 8 elements as they lie in memory, widened when they are used
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void minus_inf() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    __device__ __forceinline__ void get(float* v) const { Vec16<bf16>::unpack(r, v); }
+};
+template <> struct Raw8<float> {
+    uint4 r[2];
+    __device__ __forceinline__ void load(const float* p) {
+        r[0] = *reinterpret_cast<const uint4*>(p);
+        r[1] = *reinterpret_cast<const uint4*>(p + 4);
+    }
+    __device__ __forceinline__ void zero() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void minus_inf() {
+        r[0] = r[1] = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+    }
+    __device__ __forceinline__ void get(float* v) const {
+        Vec16<float>::unpack(r[0], v);
+        Vec16<float>::unpack(r[1], v + 4);
+    }
+};
+
+}  // namespace ssd
