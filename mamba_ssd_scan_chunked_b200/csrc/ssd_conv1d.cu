@@ -71,26 +71,6 @@ __device__ __forceinline__ int split_of(const Conv1dArgs& a, int64_t c, int64_t*
     return 2;
 }
 
-// the W - 1 inputs before token t0 of a sequence that starts at token p: kept
-// inputs where they lie before p (t0 < p: as of token p)
-template <typename IoT, int W, int VEC>
-__device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int64_t c, int64_t t0, int64_t p,
-                                            float (&win)[W][VEC]) {
-    const int64_t from = t0 < p ? p : t0;
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int64_t s = from - (W - 1) + j;
-        if (s >= p) {
-            loadv<VEC>((const IoT*)a.x + (b * a.L + s) * a.xs + c, win[j]);
-        } else if (a.init) {
-            load_state<VEC>(a.init, a.state_bf16, (b * (W - 1) + (W - 1) + (s - p)) * a.D + c, win[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
-        }
-    }
-}
-
 // VEC channels of a token as they lie in memory (8 or 16 bytes, all loads of a
 // round in flight before the first is used)
 template <typename T, int VEC> struct RawVec {
@@ -114,16 +94,69 @@ __device__ __forceinline__ void pairs(const float (&v)[N][VEC], f32x2 (&out)[N][
         for (int i = 0; i < VEC / 2; ++i) out[k][i] = f2_pack(v[k][2 * i], v[k][2 * i + 1]);
 }
 
+// the W - 1 inputs before token t0 of a sequence that starts at token p: kept
+// inputs where they lie before p (t0 < p: as of token p)
+template <typename IoT, int W, int VEC>
+__device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int64_t c, int64_t t0, int64_t p,
+                                            float (&win)[W][VEC]) {
+    const int64_t from = t0 < p ? p : t0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int64_t s = from - (W - 1) + j;
+        if (s >= p) {
+            loadv<VEC>((const IoT*)a.x + (b * a.L + s) * a.xs + c, win[j]);
+        } else if (a.init) {
+            load_state<VEC>(a.init, a.state_bf16, (b * (W - 1) + (W - 1) + (s - p)) * a.D + c, win[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+        }
+    }
+}
+
+// filter and bias of channels c .. c + VEC
+template <int W, int VEC>
+__device__ __forceinline__ void load_filter(const Conv1dArgs& a, int64_t c, f32x2 (&w)[W][VEC / 2], f32x2 (&bias)[VEC / 2]) {
+    float wf[W][VEC];
+    load_taps<W, VEC>(a.w, c, wf);
+    pairs<W, VEC>(wf, w);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) bias[i] = a.bias ? f2_pack(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
+}
+
+// the inputs before the first token of a run (of token `lead` of it, when its
+// first tokens are absent) at their places in the ring
+template <typename IoT, int W, int VEC>
+__device__ __forceinline__ void load_ring(const Conv1dArgs& a, int64_t b, int64_t c, int64_t t0, int64_t p,
+                                          f32x2 (&ring)[4][VEC / 2]) {
+    float win[W][VEC] = {};
+    load_window<IoT, W, VEC>(a, b, c, t0, p, win);
+    const int shift = t0 < p ? (int)((p - t0) & 3) : 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) ring[q][i] = 0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int slot = (4 - (W - 1) + j + shift) & 3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i)
+                if (slot == q) ring[q][i] = f2_pack(win[j][2 * i], win[j][2 * i + 1]);
+    }
+}
+
 // The forward: kFwdRound tokens' loads are in flight while the round before is
 // computed.  A run of 32 tokens reads 3 / 32 of its inputs twice and its filter
 // once per 512 bytes of input; where there are fewer threads than keep an SM's
 // loads in flight, runs of 8.
-constexpr int kFwdThreads = 128, kFwdRound = 4;
+constexpr int kFwdThreads = 128, kFwdRound = 4, kFwdVec = 4;
 
 template <typename IoT, typename YT, int W>
-__global__ void __launch_bounds__(kFwdThreads)
+__global__ void __launch_bounds__(kFwdThreads, 8)
 conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
-    constexpr int VEC = 16 / sizeof(IoT), H = VEC / 2, U = kFwdRound;
+    constexpr int VEC = kFwdVec, H = VEC / 2, U = kFwdRound;
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * kFwdThreads + threadIdx.x) * VEC;
     const int64_t bs = blockIdx.x / (unsigned)cblocks;
     const int64_t b = bs / nseg, seg = bs % nseg;
@@ -142,57 +175,75 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
     auto load = [&](int t) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u >= lead && t + u < len) next[u].load(x + (t + u) * a.xs);
+            if (t + u >= lead && t + u < len) next[u].load(x + (int64_t)(t + u) * a.xs);
     };
     load(0);
-    f32x2 w[W][H], win[W][H], bias[H];
-    {
-        float wf[W][VEC], winf[W][VEC] = {};
-        load_taps<W, VEC>(a.w, c, wf);
-        pairs<W, VEC>(wf, w);
-        load_window<IoT, W, VEC>(a, b, c, t0, p, winf);
-        pairs<W, VEC>(winf, win);
+    // the input of token t (from t0 on) lies in slot t mod 4 of the ring
+    f32x2 w[W][H], ring[4][H], bias[H];
+    load_filter<W, VEC>(a, c, w, bias);
+    load_ring<IoT, W, VEC>(a, b, c, t0, p, ring);
+    auto token = [&](int t, int u) {
+        float out[VEC];
+        next[u].get(ring[u]);
 #pragma unroll
-        for (int i = 0; i < H; ++i) bias[i] = a.bias ? f2_pack(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
+        for (int i = 0; i < H; ++i) {
+            f32x2 v = bias[i];
+#pragma unroll
+            for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], ring[(u + 4 - (W - 1) + k) % 4][i], v);
+            const float2 r = f2_get(v);
+            out[2 * i] = a.silu ? r.x * sigmoid_f32(r.x) : r.x;
+            out[2 * i + 1] = a.silu ? r.y * sigmoid_f32(r.y) : r.y;
+        }
+        storev<VEC>(y + (int64_t)(t + u) * ld, out);
+    };
+    int t = 0;
+    // absent tokens: y = 0; the ring holds the inputs before token `lead`, at its own place
+    for (; t + U <= lead; t += U) {
+        float zero[VEC] = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u) storev<VEC>(y + (int64_t)(t + u) * ld, zero);
     }
-    for (int t = 0; t < len; t += U) {
-        RawVec<IoT, VEC> now[U];
+    if (t > 0) load(t);
+    for (; t < len; t += U) {
+        if (t >= lead && t + U <= len) {
+            RawVec<IoT, VEC> ahead[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) now[u] = next[u];
-        load(t + U);
+            for (int u = 0; u < U; ++u) ahead[u] = next[u];
+            const bool more = t + 2 * U <= len;
+            if (more) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= len) break;
-            float out[VEC];
-            if (t + u >= lead) {
-                now[u].get(win[W - 1]);
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    f32x2 v = bias[i];
-#pragma unroll
-                    for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], win[k][i], v);
-                    const float2 r = f2_get(v);
-                    out[2 * i] = a.silu ? r.x * sigmoid_f32(r.x) : r.x;
-                    out[2 * i + 1] = a.silu ? r.y * sigmoid_f32(r.y) : r.y;
-                }
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                    for (int i = 0; i < H; ++i) win[k][i] = win[k + 1][i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) out[i] = 0.f;
+                for (int u = 0; u < U; ++u) ahead[u].load(x + (int64_t)(t + U + u) * a.xs);
             }
-            storev<VEC>(y + (t + u) * ld, out);
+#pragma unroll
+            for (int u = 0; u < U; ++u) token(t, u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) next[u] = ahead[u];
+            if (!more) load(t + U);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= len) break;
+                if (t + u >= lead) {
+                    token(t, u);
+                } else {
+                    float zero[VEC] = {};
+                    storev<VEC>(y + (int64_t)(t + u) * ld, zero);
+                }
+            }
+            load(t + U);
         }
     }
     if (a.final_state && seg == nseg - 1) {
+        // the last W - 1 inputs: of the tokens before `end`
+        const int end = len > lead ? len : lead;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             float f[VEC];
+            const int slot = (end + 4 - (W - 1) + j) & 3;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                const float2 r = f2_get(win[j][i]);
+                const f32x2 lo = slot & 1 ? ring[1][i] : ring[0][i], hi = slot & 1 ? ring[3][i] : ring[2][i];
+                const float2 r = f2_get(slot & 2 ? hi : lo);
                 f[2 * i] = r.x;
                 f[2 * i + 1] = r.y;
             }
@@ -235,10 +286,10 @@ conv1d_update_kernel(const Conv1dArgs a, int cblocks) {
 // the kBwdTokens tokens of its run and the W - 1 after it (whose dv its last dx
 // need), loads a round ahead.  dx of a token is complete W - 1 tokens later.  The
 // block's sums of dw and db go to one row of the partial sums.
-constexpr int kBwdWarps = 8, kBwdTokens = 32, kBwdVec = 4, kBwdRound = 4;
+constexpr int kBwdWarps = 8, kBwdTokens = 64, kBwdVec = 4, kBwdRound = 4;
 
 template <typename IoT, typename GT, int W>
-__global__ void __launch_bounds__(kBwdWarps * 32)
+__global__ void __launch_bounds__(kBwdWarps * 32, 2)
 conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
     constexpr int VEC = kBwdVec, H = VEC / 2, U = kBwdRound;
     __shared__ float sums[kBwdWarps][(W + 1) * VEC][32];
@@ -267,85 +318,98 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (t + u < left && t + u < len + W - 1) {
-                    nx[u].load(x + (t + u) * a.xs);
-                    ny[u].load(dy + (t + u) * ld);
+                    nx[u].load(x + (int64_t)(t + u) * a.xs);
+                    ny[u].load(dy + (int64_t)(t + u) * ld);
                 }
         };
         load(0);
-        f32x2 w[W][H], win[W][H], pend[W][H], bias[H];
-        {
-            float wf[W][VEC], winf[W][VEC] = {};
-            load_taps<W, VEC>(a.w, c, wf);
-            pairs<W, VEC>(wf, w);
-            load_window<IoT, W, VEC>(a, b, c, t0, 0, winf);
-            pairs<W, VEC>(winf, win);
+        // inputs, and the gradients of inputs that later tokens still add to, in rings by token mod 4
+        f32x2 w[W][H], ring[4][H], pend[4][H], bias[H];
+        load_filter<W, VEC>(a, c, w, bias);
+        load_ring<IoT, W, VEC>(a, b, c, t0, 0, ring);
 #pragma unroll
-            for (int i = 0; i < H; ++i) bias[i] = a.bias ? f2_pack(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int k = 0; k < W; ++k)
+            for (int i = 0; i < H; ++i) pend[q][i] = 0;
+        // token u of a round adds its dv to the gradients (mine: to dw and db too)
+        auto token = [&](int u, const RawVec<IoT, VEC>& xr, const RawVec<IoT, VEC>& yr, bool mine) {
+            f32x2 dv[H];
+            xr.get(ring[u]);
+            yr.get(dv);
 #pragma unroll
-                for (int i = 0; i < H; ++i) pend[k][i] = 0;
-        }
+            for (int i = 0; i < H; ++i) {
+                if (a.silu) {
+                    f32x2 v = bias[i];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], ring[(u + 4 - (W - 1) + k) % 4][i], v);
+                    const float2 r = f2_get(v);
+                    dv[i] = f2_mul(dv[i], f2_pack(silu_grad(r.x, sigmoid_f32(r.x)), silu_grad(r.y, sigmoid_f32(r.y))));
+                }
+                if (mine) {
+                    db[i] = f2_fma(dv[i], f2_pack(1.f, 1.f), db[i]);
+#pragma unroll
+                    for (int k = 0; k < W; ++k) dw[k][i] = f2_fma(dv[i], ring[(u + 4 - (W - 1) + k) % 4][i], dw[k][i]);
+                }
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) {
+                    f32x2& q = pend[(u + 4 - (W - 1) + k) % 4][i];
+                    q = f2_fma(w[k][i], dv[i], q);
+                }
+                pend[u][i] = f2_mul(w[W - 1][i], dv[i]);
+            }
+        };
+        auto ready = [&](int u, float (&g)[VEC]) {        // the gradient that token u completes
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 r = f2_get(pend[(u + 4 - (W - 1)) % 4][i]);
+                g[2 * i] = r.x;
+                g[2 * i + 1] = r.y;
+            }
+        };
         for (int t = 0; t < len + W - 1; t += U) {
-            RawVec<IoT, VEC> now[U], dyn[U];
+            RawVec<IoT, VEC> xr[U], yr[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                now[u] = nx[u];
-                dyn[u] = ny[u];
+                xr[u] = nx[u];
+                yr[u] = ny[u];
+            }
+            if (t >= U && t + 2 * U <= len) {             // all tokens and their inputs inside the run
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    nx[u].load(x + (int64_t)(t + U + u) * a.xs);
+                    ny[u].load(dy + (int64_t)(t + U + u) * ld);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float g[VEC];
+                    token(u, xr[u], yr[u], true);
+                    ready(u, g);
+                    storev<VEC>(dx + (int64_t)(t + u - (W - 1)) * a.dxs, g);
+                }
+                continue;
             }
             load(t + U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t + u >= len + W - 1) break;
                 if (t + u < left) {
-                    f32x2 dv[H];
-                    now[u].get(win[W - 1]);
-                    dyn[u].get(dv);
+                    token(u, xr[u], yr[u], t + u < len);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        if (a.silu) {
-                            f32x2 v = bias[i];
-#pragma unroll
-                            for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], win[k][i], v);
-                            const float2 r = f2_get(v);
-                            dv[i] = f2_mul(dv[i], f2_pack(silu_grad(r.x, sigmoid_f32(r.x)), silu_grad(r.y, sigmoid_f32(r.y))));
-                        }
-                        if (t + u < len) {
-                            db[i] = f2_fma(dv[i], f2_pack(1.f, 1.f), db[i]);
-#pragma unroll
-                            for (int k = 0; k < W; ++k) dw[k][i] = f2_fma(dv[i], win[k][i], dw[k][i]);
-                        }
-#pragma unroll
-                        for (int k = 0; k < W; ++k) pend[k][i] = f2_fma(w[k][i], dv[i], pend[k][i]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                        for (int i = 0; i < H; ++i) win[k][i] = win[k + 1][i];
+                    for (int i = 0; i < H; ++i) pend[u][i] = 0;
                 }
-                const int s = t + u - (W - 1);        // the input (from t0 on) whose gradient is now complete
+                const int s = t + u - (W - 1);            // the input (from t0 on) whose gradient is now complete
                 if (s >= 0 || t0 == 0) {
                     float g[VEC];
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float2 r = f2_get(pend[0][i]);
-                        g[2 * i] = r.x;
-                        g[2 * i + 1] = r.y;
-                    }
+                    ready(u, g);
                     if (a.dfinal && s >= left - (W - 1)) {
                         float f[VEC];
                         load_state<VEC>(a.dfinal, a.state_bf16, (b * (W - 1) + s - left + W - 1) * a.D + c, f);
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) g[i] += f[i];
                     }
-                    if (s >= 0) storev<VEC>(dx + s * a.dxs, g);
+                    if (s >= 0) storev<VEC>(dx + (int64_t)s * a.dxs, g);
                     else if (a.dinit) store_state<VEC>(a.dinit, a.state_bf16, (b * (W - 1) + s + W - 1) * a.D + c, g);
-                }
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k) pend[k][i] = pend[k + 1][i];
-                    pend[W - 1][i] = 0;
                 }
             }
         }
@@ -409,7 +473,7 @@ int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D) {
     } while (0)
 
 cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s) {
-    const int vec = a.io_bf16 ? 8 : 4;
+    const int vec = kFwdVec;
     const int run = fwd_run(a.batch, a.L, a.D / vec);
     const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads), nseg = (int)fwd_segments(a.L, run);
     const unsigned grid = (unsigned)(a.batch * nseg * cblocks);

@@ -10,15 +10,23 @@
 // A stream bound by HBM: a row's group is read once and kept in registers over
 // its sums (the mean first and then the squares of the differences, not their
 // expanded form, which cancels).  Items, the pairs (row, group) in memory order,
-// go to slots: `lanes` neighbouring threads each, up to a warp, or the whole
-// block.  The number of slots is a multiple of the groups, so that a slot meets
-// one group only and keeps its weights, and the sums of dw and db, in registers.
+// go to slots of `lanes` neighbouring threads, each with NV vectors of 8
+// channels: part of a warp, or several warps.  A slot's next item is loaded
+// while its present one is summed.  The number of slots is a multiple of the
+// groups, so that a slot meets one group only and keeps the sums of dw and db in
+// registers.  Without the mean the backward's two sums, of c^2 and of dn c, are
+// formed at once (mean(dn nrm) = r mean(dn c)): one exchange a row.
 #include "ssd_internal.h"
 #include "ssd_vec.cuh"
 
 namespace ssd {
 
-constexpr int kNone = 0, kSilu = 1, kAfter = 2, kBefore = 3;   // ssd_norm_activation_t
+constexpr int kSilu = 1, kAfter = 2, kBefore = 3;   // ssd_norm_activation_t (0: none)
+
+// blocks an SM: 64 registers a thread forward, 128 backward (64 with 1024 threads)
+constexpr int norm_blocks_per_sm(bool backward, int threads) {
+    return threads >= 1024 ? 1 : (backward ? 512 : 1024) / threads;
+}
 
 struct NormShape {
     int gs;          // channels of a group
@@ -28,190 +36,281 @@ struct NormShape {
     int64_t blocks, items;
 };
 
-// sum over the slot's threads; every thread gets it
-template <bool BLOCK>
-__device__ __forceinline__ float slot_sum(float v, int lanes, float* red) {
-    const int span = BLOCK ? 32 : lanes;
-    for (int o = span >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if constexpr (BLOCK) {
-        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-        __syncthreads();                       // red may still be read by the sum before
-        if ((threadIdx.x & 31) == 0) red[warp] = v;
+// Sums K values over the slot's threads; every thread gets them.  Across warps
+// the warps' sums meet in shared memory; `turn` alternates between its two
+// halves, so that one barrier an exchange is enough.
+template <int K, bool WARP>
+__device__ __forceinline__ void slot_sum(float (&v)[K], const NormShape& sh, float (*red)[32][2], int& turn) {
+    const int span = WARP ? sh.lanes : 32;
+    for (int o = span >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if constexpr (!WARP) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = sh.lanes >> 5, first = warp / per * per;
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[turn][warp][k] = v[k];
         __syncthreads();
-        v = 0.f;
-        for (int w = 0; w < nw; ++w) v += red[w];
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = lane < per ? red[turn][first + lane][k] : 0.f;
+        turn ^= 1;
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
-    return v;
 }
 
-// Loads one item and forms nrm (in u), r and silu(z)'s factors.
-template <typename XT, typename IoT, int NV, bool BLOCK>
-struct Item {
-    float u[NV][8];
-
-    __device__ __forceinline__ float normalise(const GroupNormArgs& a, const NormShape& sh, int64_t item, bool live,
-                                               int lane, float* red, float (&x)[NV][8], float (&z)[NV][8]) {
-        const int64_t row = item / a.G, g = item % a.G;
-        const XT* xp = (const XT*)a.x + item * sh.gs;
-        const IoT* zp = (const IoT*)a.z + row * a.zs + g * sh.gs;
-        float s = 0.f;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int i = (lane + q * sh.lanes) * 8;
-            const bool ok = live && i < sh.gs;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[q][j] = z[q][j] = 0.f;
-            if (ok) {
-                load8(xp + i, x[q]);
-                if (a.act >= kAfter) load8(zp + i, z[q]);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                u[q][j] = a.act == kBefore ? x[q][j] * (z[q][j] * sigmoid_f32(z[q][j])) : x[q][j];
-                s += u[q][j];
-            }
-        }
-        const float inv = 1.f / (float)sh.gs;
-        if (a.center) {
-            const float m = slot_sum<BLOCK>(s, sh.lanes, red) * inv;
-#pragma unroll
-            for (int q = 0; q < NV; ++q) {
-                const bool ok = (lane + q * sh.lanes) * 8 < sh.gs;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[q][j] = ok ? u[q][j] - m : 0.f;
-            }
-        }
-        float ss = 0.f;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(u[q][j], u[q][j], ss);
-        const float r = 1.f / sqrtf(slot_sum<BLOCK>(ss, sh.lanes, red) * inv + a.eps);
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[q][j] *= r;
-        return r;
+// where a thread stands
+template <bool WARP> struct Place {
+    int slot, lane;
+    int64_t first, step;     // the slot's first item, from one of its items to the next
+    __device__ __forceinline__ explicit Place(const NormShape& sh) {
+        slot = (int)threadIdx.x / sh.lanes;
+        lane = (int)threadIdx.x % sh.lanes;
+        first = (int64_t)blockIdx.x * sh.per_block + slot;
+        step = sh.blocks * sh.per_block;
     }
 };
 
-template <typename XT, typename IoT, typename YT, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 128)
-group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
-    __shared__ float red[32];
-    const int slot = BLOCK ? 0 : (int)threadIdx.x / sh.lanes, lane = BLOCK ? (int)threadIdx.x : (int)threadIdx.x % sh.lanes;
-    const int64_t first = (int64_t)blockIdx.x * sh.per_block + slot, step = sh.blocks * sh.per_block;
-    const int64_t base = (first % a.G) * sh.gs;
-    float w[NV][8], bias[NV][8];
+// r and nrm (in the place of u) from u; masked channels of u are 0
+template <int NV, bool WARP>
+__device__ __forceinline__ float normalise(const GroupNormArgs& a, const NormShape& sh, const Place<WARP>& at,
+                                           float (&u)[NV][8], float (*red)[32][2], int& turn) {
+    const float inv = 1.f / (float)sh.gs;
+    if (a.center) {
+        float s[1] = {0.f};
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-        const int i = (lane + q * sh.lanes) * 8;
+        for (int q = 0; q < NV; ++q)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) { w[q][j] = 1.f; bias[q][j] = 0.f; }
-        if (i < sh.gs) {
-            if (a.w) load8(a.w + base + i, w[q]);
-            if (a.bias) load8(a.bias + base + i, bias[q]);
-        }
+            for (int j = 0; j < 8; ++j) s[0] += u[q][j];
+        slot_sum<1, WARP>(s, sh, red, turn);
+        const float m = s[0] * inv;
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if ((at.lane + q * sh.lanes) * 8 < sh.gs)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[q][j] -= m;
     }
-    // every thread of a warp takes part in its sums, with or without an item
-    for (int64_t it0 = (int64_t)blockIdx.x * sh.per_block; it0 < sh.items; it0 += step) {
-        const int64_t item = it0 + slot;
-        const bool live = item < sh.items;
-        Item<XT, IoT, NV, BLOCK> t;
-        float x[NV][8], z[NV][8];
-        t.normalise(a, sh, item, live, lane, red, x, z);
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss[0] = fmaf(u[q][j], u[q][j], ss[0]);
+    slot_sum<1, WARP>(ss, sh, red, turn);
+    const float r = 1.f / sqrtf(ss[0] * inv + a.eps);
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[q][j] *= r;
+    return r;
+}
+
+template <typename XT, typename IoT, typename YT, int NV, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS, norm_blocks_per_sm(false, THREADS))
+group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
+    __shared__ float red[2][32][2];
+    const Place<WARP> at(sh);
+    const int64_t base = (at.first % a.G) * sh.gs;
+    int turn = 0;
+    Raw8<XT> nx[NV];
+    Raw8<IoT> nz[NV];
+    auto load = [&](int64_t item) {
+        const XT* xp = (const XT*)a.x + item * sh.gs;
+        const IoT* zp = (const IoT*)a.z + item / a.G * a.zs + base;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = (lane + q * sh.lanes) * 8;
-            float y[8];
+            const int i = (at.lane + q * sh.lanes) * 8;
+            nx[q].zero();
+            nz[q].zero();
+            if (item < sh.items && i < sh.gs) {
+                nx[q].load(xp + i);
+                if (a.act >= kAfter) nz[q].load(zp + i);
+            }
+        }
+    };
+    load(at.first);
+    // every thread of a block takes part in its sums, with or without an item
+    for (int64_t it0 = (int64_t)blockIdx.x * sh.per_block; it0 < sh.items; it0 += at.step) {
+        const int64_t item = it0 + at.slot;
+        float u[NV][8], gate[NV][8];
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            nx[q].get(u[q]);
+            if (a.act >= kAfter) {
+                nz[q].get(gate[q]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) gate[q][j] *= sigmoid_f32(gate[q][j]);
+                if (a.act == kBefore)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[q][j] *= gate[q][j];
+            }
+        }
+        load(item + at.step);
+        normalise<NV, WARP>(a, sh, at, u, red, turn);
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int i = (at.lane + q * sh.lanes) * 8;
+            if (item >= sh.items || i >= sh.gs) continue;
+            float w[8], y[8];
+            if (a.w) {
+                load8(a.w + base + i, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[q][j] *= w[j];
+            }
+            if (a.bias) {
+                load8(a.bias + base + i, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[q][j] += w[j];
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = fmaf(t.u[q][j], w[q][j], bias[q][j]);
-                y[j] = a.act == kSilu ? v * sigmoid_f32(v) : a.act == kAfter ? v * (z[q][j] * sigmoid_f32(z[q][j])) : v;
+                const float v = u[q][j];
+                y[j] = a.act == kSilu ? v * sigmoid_f32(v) : a.act == kAfter ? v * gate[q][j] : v;
             }
-            if (live && i < sh.gs) store8((YT*)a.y + item * sh.gs + i, y);
+            store8((YT*)a.y + item * sh.gs + i, y);
         }
     }
 }
 
-template <typename XT, typename IoT, typename GT, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 128)
+template <typename XT, typename IoT, typename GT, int NV, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS, norm_blocks_per_sm(true, THREADS))
 group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
-    __shared__ float red[32];
-    const int slot = BLOCK ? 0 : (int)threadIdx.x / sh.lanes, lane = BLOCK ? (int)threadIdx.x : (int)threadIdx.x % sh.lanes;
-    const int64_t first = (int64_t)blockIdx.x * sh.per_block + slot, step = sh.blocks * sh.per_block;
-    const int64_t base = (first % a.G) * sh.gs;
+    __shared__ float red[2][32][2];
+    const Place<WARP> at(sh);
+    const int64_t base = (at.first % a.G) * sh.gs;
     const float inv = 1.f / (float)sh.gs;
+    int turn = 0;
     float dw[NV][8], db[NV][8];
 #pragma unroll
     for (int q = 0; q < NV; ++q)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[q][j] = db[q][j] = 0.f;
-    for (int64_t it0 = (int64_t)blockIdx.x * sh.per_block; it0 < sh.items; it0 += step) {
-        const int64_t item = it0 + slot;
-        const bool live = item < sh.items;
-        Item<XT, IoT, NV, BLOCK> t;
-        float x[NV][8], z[NV][8], dn[NV][8];
-        const float r = t.normalise(a, sh, item, live, lane, red, x, z);
-        float s0 = 0.f, s1 = 0.f;
+    Raw8<XT> nx[NV];
+    Raw8<IoT> nz[NV], ny[NV];
+    auto load = [&](int64_t item) {
+        const XT* xp = (const XT*)a.x + item * sh.gs;
+        const IoT* yp = (const IoT*)a.dy + item * sh.gs;
+        const IoT* zp = (const IoT*)a.z + item / a.G * a.zs + base;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = (lane + q * sh.lanes) * 8;
-            const bool ok = live && i < sh.gs;
-            float w[8], bias[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) { dn[q][j] = 0.f; w[j] = 1.f; bias[j] = 0.f; }
-            if (ok) {
-                load8((const IoT*)a.dy + item * sh.gs + i, dn[q]);
-                if (a.w) load8(a.w + base + i, w);
-                if (a.bias) load8(a.bias + base + i, bias);
+            const int i = (at.lane + q * sh.lanes) * 8;
+            nx[q].zero();
+            nz[q].zero();
+            ny[q].zero();
+            if (item < sh.items && i < sh.gs) {
+                nx[q].load(xp + i);
+                ny[q].load(yp + i);
+                if (a.act >= kAfter) nz[q].load(zp + i);
             }
-            float dz[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float dv = dn[q][j];
-                const float v = fmaf(t.u[q][j], w[j], bias[j]);
-                if (a.act == kSilu) {
-                    dv *= silu_grad(v, sigmoid_f32(v));
-                } else if (a.act == kAfter) {
-                    dz[j] = dv * v * silu_grad(z[q][j], sigmoid_f32(z[q][j]));
-                    dv *= z[q][j] * sigmoid_f32(z[q][j]);
-                }
-                dw[q][j] = fmaf(dv, t.u[q][j], dw[q][j]);
-                db[q][j] += dv;
-                dn[q][j] = dv * w[j];
-                s0 += dn[q][j];
-                s1 = fmaf(dn[q][j], t.u[q][j], s1);
-            }
-            if (a.act == kAfter && ok) store8((GT*)a.dz + item * sh.gs + i, dz);
         }
-        s1 = slot_sum<BLOCK>(s1, sh.lanes, red) * inv;
-        s0 = a.center ? slot_sum<BLOCK>(s0, sh.lanes, red) * inv : 0.f;
+    };
+    load(at.first);
+    for (int64_t it0 = (int64_t)blockIdx.x * sh.per_block; it0 < sh.items; it0 += at.step) {
+        const int64_t item = it0 + at.slot;
+        // s: silu(z); t: what dz takes beside du (x silu'(z)) or beside v (dy silu'(z))
+        float u[NV][8], dn[NV][8], s[NV][8], t[NV][8], r, s0 = 0.f, s1;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = (lane + q * sh.lanes) * 8;
-            float dx[8], dz[8];
+            nx[q].get(u[q]);
+            ny[q].get(dn[q]);
+            if (a.act >= kAfter) {
+                float z[8];
+                nz[q].get(z);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float du = r * (dn[q][j] - s0 - t.u[q][j] * s1);
-                dx[j] = du;
-                if (a.act == kBefore) {
-                    dx[j] = du * (z[q][j] * sigmoid_f32(z[q][j]));
-                    dz[j] = du * x[q][j] * silu_grad(z[q][j], sigmoid_f32(z[q][j]));
+                for (int j = 0; j < 8; ++j) {
+                    const float g = sigmoid_f32(z[j]);
+                    s[q][j] = z[j] * g;
+                    t[q][j] = silu_grad(z[j], g) * (a.act == kBefore ? u[q][j] : dn[q][j]);
+                    if (a.act == kBefore) u[q][j] *= s[q][j];
+                    else dn[q][j] *= s[q][j];               // dv
                 }
             }
-            if (live && i < sh.gs) {
-                store8((GT*)a.dx + item * sh.gs + i, dx);
-                if (a.act == kBefore) store8((GT*)a.dz + item * sh.gs + i, dz);
+        }
+        load(item + at.step);
+        if (!a.center && a.act != kSilu) {
+            float sums[2] = {0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                const int i = (at.lane + q * sh.lanes) * 8;
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 1.f;
+                if (a.w && i < sh.gs) load8(a.w + base + i, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sums[0] = fmaf(u[q][j], u[q][j], sums[0]);
+                    sums[1] = fmaf(dn[q][j] * w[j], u[q][j], sums[1]);
+                }
             }
+            slot_sum<2, WARP>(sums, sh, red, turn);
+            r = 1.f / sqrtf(sums[0] * inv + a.eps);
+            s1 = r * sums[1] * inv;
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[q][j] *= r;
+        } else {
+            r = normalise<NV, WARP>(a, sh, at, u, red, turn);
+            float sums[2] = {0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                const int i = (at.lane + q * sh.lanes) * 8;
+                float w[8], bias[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) { w[j] = 1.f; bias[j] = 0.f; }
+                if (a.w && i < sh.gs) load8(a.w + base + i, w);
+                if (a.bias && a.act == kSilu && i < sh.gs) load8(a.bias + base + i, bias);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (a.act == kSilu) {
+                        const float v = fmaf(u[q][j], w[j], bias[j]);
+                        dn[q][j] *= silu_grad(v, sigmoid_f32(v));
+                    }
+                    sums[0] = fmaf(dn[q][j], w[j], sums[0]);
+                    sums[1] = fmaf(dn[q][j] * w[j], u[q][j], sums[1]);
+                }
+            }
+            slot_sum<2, WARP>(sums, sh, red, turn);
+            s0 = a.center ? sums[0] * inv : 0.f;
+            s1 = sums[1] * inv;
+        }
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int i = (at.lane + q * sh.lanes) * 8;
+            if (item >= sh.items || i >= sh.gs) continue;
+            float w[8], g[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 1.f;
+            if (a.w) load8(a.w + base + i, w);
+            if (a.act == kAfter) {
+                float bias[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+                if (a.bias) load8(a.bias + base + i, bias);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = t[q][j] * fmaf(u[q][j], w[j], bias[j]);
+                store8((GT*)a.dz + item * sh.gs + i, g);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[q][j] = fmaf(dn[q][j], u[q][j], dw[q][j]);
+                db[q][j] += dn[q][j];
+                g[j] = r * (fmaf(dn[q][j], w[j], -s0) - u[q][j] * s1);          // du
+                if (a.act == kBefore) {
+                    t[q][j] *= g[j];
+                    g[j] *= s[q][j];
+                }
+            }
+            store8((GT*)a.dx + item * sh.gs + i, g);
+            if (a.act == kBefore) store8((GT*)a.dz + item * sh.gs + i, t[q]);
         }
     }
     // slot q's sums: row q / G of [slots / G][C]
-    float* part = a.ws + first * sh.gs;
-    const int64_t all = step * sh.gs;
+    float* part = a.ws + at.first * sh.gs;
+    const int64_t all = at.step * sh.gs;
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
-        const int i = (lane + q * sh.lanes) * 8;
+        const int i = (at.lane + q * sh.lanes) * 8;
         if (i >= sh.gs) continue;
         if (a.dw) store8(part + i, dw[q]);
         if (a.db) store8(part + all + i, db[q]);
@@ -226,77 +325,81 @@ __global__ void group_norm_zero_kernel(float* dw, float* db, int64_t n) {
     }
 }
 
-// Slots: one vector of 8 channels a lane up to 32 lanes, then 4 a lane in a
-// warp, then a block with 2 a lane.
-static NormShape norm_shape(int64_t rows, int64_t C, int64_t G, int* nv, bool* block) {
+// Slots: one vector of 8 channels a lane, up to 32 lanes of a warp, then whole
+// warps, as many slots a block as make 512 threads; two vectors a lane beyond 8192
+// channels (backward: beyond 4096, whose sums and terms take 128 registers a lane).
+enum class NormClass { kWarp, kBlock512, kBlock1024, kBlock2 };
+
+static NormShape norm_shape(int64_t rows, int64_t C, int64_t G, bool backward, NormClass* cls) {
     NormShape sh{};
     sh.gs = (int)(C / G);
     const int vecs = sh.gs / 8;
-    if (vecs <= 128) {
-        *nv = vecs <= 32 ? 1 : 4;
-        *block = false;
+    if (vecs <= 32) {
+        *cls = NormClass::kWarp;
         sh.lanes = 1;
-        while (sh.lanes < 32 && sh.lanes < vecs) sh.lanes *= 2;
-        sh.threads = 128;
-        sh.per_block = 128 / sh.lanes;
+        while (sh.lanes < vecs) sh.lanes *= 2;
+        sh.threads = 256;
+        sh.per_block = 256 / sh.lanes;
     } else {
-        *nv = 2;
-        *block = true;
-        sh.lanes = (vecs / 2 + 31) / 32 * 32;
-        while (sh.lanes * 2 < vecs) sh.lanes += 32;
-        sh.threads = sh.lanes;
-        sh.per_block = 1;
+        *cls = vecs <= 512 ? NormClass::kBlock512 : vecs <= 1024 ? NormClass::kBlock1024 : NormClass::kBlock2;
+        const int per_lane = *cls == NormClass::kBlock2 || (backward && *cls == NormClass::kBlock1024) ? 2 : 1;
+        sh.lanes = ((vecs + per_lane - 1) / per_lane + 31) / 32 * 32;
+        sh.per_block = sh.lanes <= 512 ? 512 / sh.lanes : 1;
+        sh.threads = sh.lanes * sh.per_block;
     }
     sh.items = rows * G;
-    // blocks: a multiple of `unit`, so that all slots together are a multiple of G
+    // blocks: a multiple of `unit`, so that all slots together are a multiple of G; as many as fit on the
+    // machine at once, so that each keeps its next item's loads in flight
     int64_t x = G, y = sh.per_block;
     while (y) { const int64_t m = x % y; x = y; y = m; }
     const int64_t unit = G / x, want = (sh.items + sh.per_block - 1) / sh.per_block;
-    const int64_t most = (int64_t)148 * (2048 / sh.threads);
-    const int64_t n = want < most ? want : most;
+    const bool half = *cls == NormClass::kBlock512 || (backward && *cls == NormClass::kBlock1024);
+    const int64_t most = (int64_t)148 * norm_blocks_per_sm(backward, *cls == NormClass::kWarp ? 256 : half ? 512 : 1024);
+    const int64_t n = want < most ? want : most / unit > 0 ? most / unit * unit : unit;
     sh.blocks = (n + unit - 1) / unit * unit;
-    if (sh.blocks < unit) sh.blocks = unit;
     return sh;
 }
 
 size_t group_norm_bwd_workspace(int64_t rows, int64_t C, int64_t G) {
-    int nv; bool block;
-    const NormShape sh = norm_shape(rows, C, G, &nv, &block);
+    NormClass cls;
+    const NormShape sh = norm_shape(rows, C, G, true, &cls);
     return rows ? (size_t)sh.blocks * sh.per_block * sh.gs * 2 * sizeof(float) : 0;
 }
 
+template <typename X, typename I, typename Y> struct NormFwd {
+    static void go(const GroupNormArgs& a, const NormShape& sh, NormClass cls, cudaStream_t s) {
+        const unsigned grid = (unsigned)sh.blocks;
+        if (cls == NormClass::kWarp) group_norm_fwd_kernel<X, I, Y, 1, true, 256><<<grid, sh.threads, 0, s>>>(a, sh);
+        else if (cls == NormClass::kBlock512) group_norm_fwd_kernel<X, I, Y, 1, false, 512><<<grid, sh.threads, 0, s>>>(a, sh);
+        else if (cls == NormClass::kBlock1024) group_norm_fwd_kernel<X, I, Y, 1, false, 1024><<<grid, sh.threads, 0, s>>>(a, sh);
+        else group_norm_fwd_kernel<X, I, Y, 2, false, 1024><<<grid, sh.threads, 0, s>>>(a, sh);
+    }
+};
+template <typename X, typename I, typename Y> struct NormBwd {
+    static void go(const GroupNormArgs& a, const NormShape& sh, NormClass cls, cudaStream_t s) {
+        const unsigned grid = (unsigned)sh.blocks;
+        if (cls == NormClass::kWarp) group_norm_bwd_kernel<X, I, Y, 1, true, 256><<<grid, sh.threads, 0, s>>>(a, sh);
+        else if (cls == NormClass::kBlock512) group_norm_bwd_kernel<X, I, Y, 1, false, 512><<<grid, sh.threads, 0, s>>>(a, sh);
+        else if (cls == NormClass::kBlock1024) group_norm_bwd_kernel<X, I, Y, 2, false, 512><<<grid, sh.threads, 0, s>>>(a, sh);
+        else group_norm_bwd_kernel<X, I, Y, 2, false, 1024><<<grid, sh.threads, 0, s>>>(a, sh);
+    }
+};
+
 template <template <typename, typename, typename> class F>
-static void dispatch_types(const GroupNormArgs& a, const NormShape& sh, int nv, bool block, cudaStream_t s) {
+static void dispatch_types(const GroupNormArgs& a, const NormShape& sh, NormClass cls, cudaStream_t s) {
     if (a.x_bf16) {
-        if (a.io_bf16) { if (a.y_bf16) F<bf16, bf16, bf16>::go(a, sh, nv, block, s); else F<bf16, bf16, float>::go(a, sh, nv, block, s); }
-        else { if (a.y_bf16) F<bf16, float, bf16>::go(a, sh, nv, block, s); else F<bf16, float, float>::go(a, sh, nv, block, s); }
+        if (a.io_bf16) { if (a.y_bf16) F<bf16, bf16, bf16>::go(a, sh, cls, s); else F<bf16, bf16, float>::go(a, sh, cls, s); }
+        else { if (a.y_bf16) F<bf16, float, bf16>::go(a, sh, cls, s); else F<bf16, float, float>::go(a, sh, cls, s); }
     } else {
-        if (a.io_bf16) { if (a.y_bf16) F<float, bf16, bf16>::go(a, sh, nv, block, s); else F<float, bf16, float>::go(a, sh, nv, block, s); }
-        else { if (a.y_bf16) F<float, float, bf16>::go(a, sh, nv, block, s); else F<float, float, float>::go(a, sh, nv, block, s); }
+        if (a.io_bf16) { if (a.y_bf16) F<float, bf16, bf16>::go(a, sh, cls, s); else F<float, bf16, float>::go(a, sh, cls, s); }
+        else { if (a.y_bf16) F<float, float, bf16>::go(a, sh, cls, s); else F<float, float, float>::go(a, sh, cls, s); }
     }
 }
 
-template <typename X, typename I, typename Y> struct Fwd {
-    static void go(const GroupNormArgs& a, const NormShape& sh, int nv, bool block, cudaStream_t s) {
-        const unsigned grid = (unsigned)sh.blocks;
-        if (block) group_norm_fwd_kernel<X, I, Y, 2, true><<<grid, sh.threads, 0, s>>>(a, sh);
-        else if (nv == 1) group_norm_fwd_kernel<X, I, Y, 1, false><<<grid, sh.threads, 0, s>>>(a, sh);
-        else group_norm_fwd_kernel<X, I, Y, 4, false><<<grid, sh.threads, 0, s>>>(a, sh);
-    }
-};
-template <typename X, typename I, typename Y> struct Bwd {
-    static void go(const GroupNormArgs& a, const NormShape& sh, int nv, bool block, cudaStream_t s) {
-        const unsigned grid = (unsigned)sh.blocks;
-        if (block) group_norm_bwd_kernel<X, I, Y, 2, true><<<grid, sh.threads, 0, s>>>(a, sh);
-        else if (nv == 1) group_norm_bwd_kernel<X, I, Y, 1, false><<<grid, sh.threads, 0, s>>>(a, sh);
-        else group_norm_bwd_kernel<X, I, Y, 4, false><<<grid, sh.threads, 0, s>>>(a, sh);
-    }
-};
-
 cudaError_t launch_group_norm_fwd(const GroupNormArgs& a, cudaStream_t s) {
-    int nv; bool block;
-    const NormShape sh = norm_shape(a.rows, a.C, a.G, &nv, &block);
-    dispatch_types<Fwd>(a, sh, nv, block, s);
+    NormClass cls;
+    const NormShape sh = norm_shape(a.rows, a.C, a.G, false, &cls);
+    dispatch_types<NormFwd>(a, sh, cls, s);
     return cudaGetLastError();
 }
 
@@ -306,9 +409,9 @@ cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s) {
         group_norm_zero_kernel<<<(unsigned)((a.C + 255) / 256), 256, 0, s>>>(a.dw, a.db, a.C);
         return cudaGetLastError();
     }
-    int nv; bool block;
-    const NormShape sh = norm_shape(a.rows, a.C, a.G, &nv, &block);
-    dispatch_types<Bwd>(a, sh, nv, block, s);
+    NormClass cls;
+    const NormShape sh = norm_shape(a.rows, a.C, a.G, true, &cls);
+    dispatch_types<NormBwd>(a, sh, cls, s);
     cudaError_t e = cudaGetLastError();
     const int64_t rows = sh.blocks * sh.per_block / a.G;
     if (e == cudaSuccess && a.dw) e = launch_column_sum(a.ws, rows, a.C, a.C, a.dw, false, s);
