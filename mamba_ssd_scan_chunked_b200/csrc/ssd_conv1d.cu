@@ -14,44 +14,20 @@
 
 namespace ssd {
 
-// VEC consecutive elements (VEC * sizeof(T) is 8, 16 or 32 bytes) to and from fp32
-template <int VEC> __device__ __forceinline__ void loadv(const bf16* p, float* v) {
-    if constexpr (VEC == 8) {
-        load8(p, v);
-    } else {
-        const uint2 r = *reinterpret_cast<const uint2*>(p);
-        v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xffff0000u);
-        v[2] = __uint_as_float(r.y << 16); v[3] = __uint_as_float(r.y & 0xffff0000u);
-    }
+constexpr int VEC = 4;    // channels of a thread: 8 or 16 bytes a token
+
+// the kept inputs, whose dtype is known at run time only
+__device__ __forceinline__ void load_state(const void* p, bool is_bf16, int64_t i, float* v) {
+    if (is_bf16) load4((const bf16*)p + i, v);
+    else load4((const float*)p + i, v);
 }
-template <int VEC> __device__ __forceinline__ void loadv(const float* p, float* v) {
-    if constexpr (VEC == 8) load8(p, v);
-    else Vec16<float>::load(p, v);
-}
-template <int VEC> __device__ __forceinline__ void storev(bf16* p, const float* v) {
-    if constexpr (VEC == 8) {
-        store8(p, v);
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                                  *reinterpret_cast<const uint32_t*>(&b));
-    }
-}
-template <int VEC> __device__ __forceinline__ void storev(float* p, const float* v) {
-    if constexpr (VEC == 8) store8(p, v);
-    else Vec16<float>::store(p, v);
-}
-template <int VEC> __device__ __forceinline__ void load_state(const void* p, bool is_bf16, int64_t i, float* v) {
-    if (is_bf16) loadv<VEC>((const bf16*)p + i, v);
-    else loadv<VEC>((const float*)p + i, v);
-}
-template <int VEC> __device__ __forceinline__ void store_state(void* p, bool is_bf16, int64_t i, const float* v) {
-    if (is_bf16) storev<VEC>((bf16*)p + i, v);
-    else storev<VEC>((float*)p + i, v);
+__device__ __forceinline__ void store_state(void* p, bool is_bf16, int64_t i, const float* v) {
+    if (is_bf16) store4((bf16*)p + i, v);
+    else store4((float*)p + i, v);
 }
 
 // weight [D][W] of channels c .. c + VEC as w[k][i]
-template <int W, int VEC>
+template <int W>
 __device__ __forceinline__ void load_taps(const float* w, int64_t c, float (&out)[W][VEC]) {
     float raw[W * VEC];
 #pragma unroll
@@ -71,9 +47,9 @@ __device__ __forceinline__ int split_of(const Conv1dArgs& a, int64_t c, int64_t*
     return 2;
 }
 
-// VEC channels of a token as they lie in memory (8 or 16 bytes, all loads of a
-// round in flight before the first is used)
-template <typename T, int VEC> struct RawVec {
+// VEC channels of a token as they lie in memory (all loads of a round in flight
+// before the first is used)
+template <typename T> struct Raw4 {
     typename std::conditional<sizeof(T) * VEC == 16, uint4, uint2>::type r;
     __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const decltype(r)*>(p); }
     __device__ __forceinline__ void get(f32x2 (&v)[VEC / 2]) const {
@@ -86,17 +62,9 @@ template <typename T, int VEC> struct RawVec {
     }
 };
 
-template <int N, int VEC>
-__device__ __forceinline__ void pairs(const float (&v)[N][VEC], f32x2 (&out)[N][VEC / 2]) {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) out[k][i] = f2_pack(v[k][2 * i], v[k][2 * i + 1]);
-}
-
 // the W - 1 inputs before token t0 of a sequence that starts at token p: kept
 // inputs where they lie before p (t0 < p: as of token p)
-template <typename IoT, int W, int VEC>
+template <typename IoT, int W>
 __device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int64_t c, int64_t t0, int64_t p,
                                             float (&win)[W][VEC]) {
     const int64_t from = t0 < p ? p : t0;
@@ -104,9 +72,9 @@ __device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int6
     for (int j = 0; j < W - 1; ++j) {
         const int64_t s = from - (W - 1) + j;
         if (s >= p) {
-            loadv<VEC>((const IoT*)a.x + (b * a.L + s) * a.xs + c, win[j]);
+            load4((const IoT*)a.x + (b * a.L + s) * a.xs + c, win[j]);
         } else if (a.init) {
-            load_state<VEC>(a.init, a.state_bf16, (b * (W - 1) + (W - 1) + (s - p)) * a.D + c, win[j]);
+            load_state(a.init, a.state_bf16, (b * (W - 1) + (W - 1) + (s - p)) * a.D + c, win[j]);
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
@@ -115,22 +83,26 @@ __device__ __forceinline__ void load_window(const Conv1dArgs& a, int64_t b, int6
 }
 
 // filter and bias of channels c .. c + VEC
-template <int W, int VEC>
+template <int W>
 __device__ __forceinline__ void load_filter(const Conv1dArgs& a, int64_t c, f32x2 (&w)[W][VEC / 2], f32x2 (&bias)[VEC / 2]) {
     float wf[W][VEC];
-    load_taps<W, VEC>(a.w, c, wf);
-    pairs<W, VEC>(wf, w);
+    load_taps<W>(a.w, c, wf);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k][i] = f2_pack(wf[k][2 * i], wf[k][2 * i + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) bias[i] = a.bias ? f2_pack(a.bias[c + 2 * i], a.bias[c + 2 * i + 1]) : 0;
 }
 
 // the inputs before the first token of a run (of token `lead` of it, when its
 // first tokens are absent) at their places in the ring
-template <typename IoT, int W, int VEC>
+template <typename IoT, int W>
 __device__ __forceinline__ void load_ring(const Conv1dArgs& a, int64_t b, int64_t c, int64_t t0, int64_t p,
                                           f32x2 (&ring)[4][VEC / 2]) {
     float win[W][VEC] = {};
-    load_window<IoT, W, VEC>(a, b, c, t0, p, win);
+    load_window<IoT, W>(a, b, c, t0, p, win);
     const int shift = t0 < p ? (int)((p - t0) & 3) : 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -151,12 +123,12 @@ __device__ __forceinline__ void load_ring(const Conv1dArgs& a, int64_t b, int64_
 // computed.  A run of 32 tokens reads 3 / 32 of its inputs twice and its filter
 // once per 512 bytes of input; where there are fewer threads than keep an SM's
 // loads in flight, runs of 8.
-constexpr int kFwdThreads = 128, kFwdRound = 4, kFwdVec = 4;
+constexpr int kFwdThreads = 128, kFwdRound = 4;
 
 template <typename IoT, typename YT, int W>
 __global__ void __launch_bounds__(kFwdThreads, 8)
 conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
-    constexpr int VEC = kFwdVec, H = VEC / 2, U = kFwdRound;
+    constexpr int H = VEC / 2, U = kFwdRound;
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * kFwdThreads + threadIdx.x) * VEC;
     const int64_t bs = blockIdx.x / (unsigned)cblocks;
     const int64_t b = bs / nseg, seg = bs % nseg;
@@ -171,7 +143,7 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
     const IoT* x = (const IoT*)a.x + (b * a.L + t0) * a.xs + c;
     const int len = (int)(t1 - t0), lead = t0 < p ? (int)((p < t1 ? p : t1) - t0) : 0;   // lead: absent tokens
 
-    RawVec<IoT, VEC> next[U];
+    Raw4<IoT> next[U];
     auto load = [&](int t) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -180,8 +152,8 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
     load(0);
     // the input of token t (from t0 on) lies in slot t mod 4 of the ring
     f32x2 w[W][H], ring[4][H], bias[H];
-    load_filter<W, VEC>(a, c, w, bias);
-    load_ring<IoT, W, VEC>(a, b, c, t0, p, ring);
+    load_filter<W>(a, c, w, bias);
+    load_ring<IoT, W>(a, b, c, t0, p, ring);
     auto token = [&](int t, int u) {
         float out[VEC];
         next[u].get(ring[u]);
@@ -194,19 +166,19 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
             out[2 * i] = a.silu ? r.x * sigmoid_f32(r.x) : r.x;
             out[2 * i + 1] = a.silu ? r.y * sigmoid_f32(r.y) : r.y;
         }
-        storev<VEC>(y + (int64_t)(t + u) * ld, out);
+        store4(y + (int64_t)(t + u) * ld, out);
     };
     int t = 0;
     // absent tokens: y = 0; the ring holds the inputs before token `lead`, at its own place
     for (; t + U <= lead; t += U) {
         float zero[VEC] = {};
 #pragma unroll
-        for (int u = 0; u < U; ++u) storev<VEC>(y + (int64_t)(t + u) * ld, zero);
+        for (int u = 0; u < U; ++u) store4(y + (int64_t)(t + u) * ld, zero);
     }
     if (t > 0) load(t);
     for (; t < len; t += U) {
         if (t >= lead && t + U <= len) {
-            RawVec<IoT, VEC> ahead[U];
+            Raw4<IoT> ahead[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) ahead[u] = next[u];
             const bool more = t + 2 * U <= len;
@@ -227,7 +199,7 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
                     token(t, u);
                 } else {
                     float zero[VEC] = {};
-                    storev<VEC>(y + (int64_t)(t + u) * ld, zero);
+                    store4(y + (int64_t)(t + u) * ld, zero);
                 }
             }
             load(t + U);
@@ -247,51 +219,62 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
                 f[2 * i] = r.x;
                 f[2 * i + 1] = r.y;
             }
-            store_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, f);
+            store_state(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, f);
         }
     }
 }
 
-// One token: a thread owns VEC channels of a sequence, so its state is read and
-// written by no other thread.
-template <typename IoT, typename YT, int W>
+// One token: a thread owns VEC channels of NB sequences, whose state is read and
+// written by no other thread; all loads are in flight before the first is used, and
+// the filter, larger than a sequence's inputs, is fetched once for NB of them.
+template <typename IoT, typename YT, int W, int NB>
 __global__ void __launch_bounds__(kFwdThreads)
 conv1d_update_kernel(const Conv1dArgs a, int cblocks) {
-    constexpr int VEC = 16 / sizeof(IoT);
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * kFwdThreads + threadIdx.x) * VEC;
-    const int64_t b = blockIdx.x / (unsigned)cblocks;
+    const int64_t b0 = (int64_t)(blockIdx.x / (unsigned)cblocks) * NB;
     if (c >= a.D) return;
-    float w[W][VEC], win[W][VEC], out[VEC];
-    loadv<VEC>((const IoT*)a.x + b * a.xs + c, win[W - 1]);
+    float win[NB][W][VEC] = {};
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        load_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, win[j]);
-    load_taps<W, VEC>(a.w, c, w);
+    for (int u = 0; u < NB; ++u) {
+        if (b0 + u >= a.batch) break;
+        load4((const IoT*)a.x + (b0 + u) * a.xs + c, win[u][W - 1]);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        float v = a.bias ? a.bias[c + i] : 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[k][i], v);
-        out[i] = a.silu ? v * sigmoid_f32(v) : v;
+        for (int j = 0; j < W - 1; ++j)
+            load_state(a.final_state, a.state_bf16, ((b0 + u) * (W - 1) + j) * a.D + c, win[u][j]);
     }
+    float w[W][VEC], bias[VEC] = {};
+    load_taps<W>(a.w, c, w);
+    if (a.bias) Vec16<float>::load(a.bias + c, bias);
     int64_t ld, at;
     const int which = split_of(a, c, &ld, &at);
-    storev<VEC>((YT*)a.y[which] + b * ld + at, out);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        store_state<VEC>(a.final_state, a.state_bf16, (b * (W - 1) + j) * a.D + c, win[j + 1]);
+    for (int u = 0; u < NB; ++u) {
+        if (b0 + u >= a.batch) break;
+        float out[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            float v = bias[i];
+#pragma unroll
+            for (int k = 0; k < W; ++k) v = fmaf(w[k][i], win[u][k][i], v);
+            out[i] = a.silu ? v * sigmoid_f32(v) : v;
+        }
+        store4((YT*)a.y[which] + (b0 + u) * ld + at, out);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            store_state(a.final_state, a.state_bf16, ((b0 + u) * (W - 1) + j) * a.D + c, win[u][j + 1]);
+    }
 }
 
 // Backward.  A block is 32 lanes (4 channels each) x 8 warps; warp q walks over
 // the kBwdTokens tokens of its run and the W - 1 after it (whose dv its last dx
 // need), loads a round ahead.  dx of a token is complete W - 1 tokens later.  The
 // block's sums of dw and db go to one row of the partial sums.
-constexpr int kBwdWarps = 8, kBwdTokens = 64, kBwdVec = 4, kBwdRound = 4;
+constexpr int kBwdWarps = 8, kBwdTokens = 64, kBwdRound = 4;
 
 template <typename IoT, typename GT, int W>
 __global__ void __launch_bounds__(kBwdWarps * 32, 2)
 conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
-    constexpr int VEC = kBwdVec, H = VEC / 2, U = kBwdRound;
+    constexpr int H = VEC / 2, U = kBwdRound;
     __shared__ float sums[kBwdWarps][(W + 1) * VEC][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * 32 + lane) * VEC;
@@ -313,7 +296,7 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
         GT* dx = (GT*)a.dx + (b * a.L + t0) * a.dxs + c;
         const int left = a.L - t0 < (1 << 20) ? (int)(a.L - t0) : 1 << 20;   // tokens from t0 on
         const int len = left < kBwdTokens ? left : kBwdTokens;
-        RawVec<IoT, VEC> nx[U], ny[U];
+        Raw4<IoT> nx[U], ny[U];
         auto load = [&](int t) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -325,14 +308,14 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
         load(0);
         // inputs, and the gradients of inputs that later tokens still add to, in rings by token mod 4
         f32x2 w[W][H], ring[4][H], pend[4][H], bias[H];
-        load_filter<W, VEC>(a, c, w, bias);
-        load_ring<IoT, W, VEC>(a, b, c, t0, 0, ring);
+        load_filter<W>(a, c, w, bias);
+        load_ring<IoT, W>(a, b, c, t0, 0, ring);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int i = 0; i < H; ++i) pend[q][i] = 0;
         // token u of a round adds its dv to the gradients (mine: to dw and db too)
-        auto token = [&](int u, const RawVec<IoT, VEC>& xr, const RawVec<IoT, VEC>& yr, bool mine) {
+        auto token = [&](int u, const Raw4<IoT>& xr, const Raw4<IoT>& yr, bool mine) {
             f32x2 dv[H];
             xr.get(ring[u]);
             yr.get(dv);
@@ -367,7 +350,7 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
             }
         };
         for (int t = 0; t < len + W - 1; t += U) {
-            RawVec<IoT, VEC> xr[U], yr[U];
+            Raw4<IoT> xr[U], yr[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 xr[u] = nx[u];
@@ -384,7 +367,7 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
                     float g[VEC];
                     token(u, xr[u], yr[u], true);
                     ready(u, g);
-                    storev<VEC>(dx + (int64_t)(t + u - (W - 1)) * a.dxs, g);
+                    store4(dx + (int64_t)(t + u - (W - 1)) * a.dxs, g);
                 }
                 continue;
             }
@@ -404,12 +387,12 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
                     ready(u, g);
                     if (a.dfinal && s >= left - (W - 1)) {
                         float f[VEC];
-                        load_state<VEC>(a.dfinal, a.state_bf16, (b * (W - 1) + s - left + W - 1) * a.D + c, f);
+                        load_state(a.dfinal, a.state_bf16, (b * (W - 1) + s - left + W - 1) * a.D + c, f);
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) g[i] += f[i];
                     }
-                    if (s >= 0) storev<VEC>(dx + (int64_t)s * a.dxs, g);
-                    else if (a.dinit) store_state<VEC>(a.dinit, a.state_bf16, (b * (W - 1) + s + W - 1) * a.D + c, g);
+                    if (s >= 0) store4(dx + (int64_t)s * a.dxs, g);
+                    else if (a.dinit) store_state(a.dinit, a.state_bf16, (b * (W - 1) + s + W - 1) * a.D + c, g);
                 }
             }
         }
@@ -473,9 +456,8 @@ int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D) {
     } while (0)
 
 cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s) {
-    const int vec = kFwdVec;
-    const int run = fwd_run(a.batch, a.L, a.D / vec);
-    const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads), nseg = (int)fwd_segments(a.L, run);
+    const int run = fwd_run(a.batch, a.L, a.D / VEC);
+    const int cblocks = (int)((a.D / VEC + kFwdThreads - 1) / kFwdThreads), nseg = (int)fwd_segments(a.L, run);
     const unsigned grid = (unsigned)(a.batch * nseg * cblocks);
 #define FN(IO, Y, W_) conv1d_fwd_kernel<IO, Y, W_><<<grid, kFwdThreads, 0, s>>>(a, cblocks, nseg, run)
     CONV1D_DISPATCH(FN);
@@ -484,12 +466,18 @@ cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_conv1d_update(const Conv1dArgs& a, cudaStream_t s) {
-    const int vec = a.io_bf16 ? 8 : 4;
-    const int cblocks = (int)((a.D / vec + kFwdThreads - 1) / kFwdThreads);
-    const unsigned grid = (unsigned)(a.batch * cblocks);
-#define FN(IO, Y, W_) conv1d_update_kernel<IO, Y, W_><<<grid, kFwdThreads, 0, s>>>(a, cblocks)
-    CONV1D_DISPATCH(FN);
+    const int cblocks = (int)((a.D / VEC + kFwdThreads - 1) / kFwdThreads);
+    // four sequences a thread once that still leaves 512 threads an SM
+    const int64_t quads = (a.batch + 3) / 4 * cblocks;
+    if (quads >= 148 * 4) {
+#define FN(IO, Y, W_) conv1d_update_kernel<IO, Y, W_, 4><<<(unsigned)quads, kFwdThreads, 0, s>>>(a, cblocks)
+        CONV1D_DISPATCH(FN);
 #undef FN
+    } else {
+#define FN(IO, Y, W_) conv1d_update_kernel<IO, Y, W_, 1><<<(unsigned)(a.batch * cblocks), kFwdThreads, 0, s>>>(a, cblocks)
+        CONV1D_DISPATCH(FN);
+#undef FN
+    }
     return cudaGetLastError();
 }
 
@@ -499,7 +487,7 @@ cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s) {
         conv1d_zero_kernel<<<(unsigned)((nw + a.D + 255) / 256), 256, 0, s>>>(a.dw, a.db, nw, a.D);
         return cudaGetLastError();
     }
-    const int cblocks = (int)((a.D / kBwdVec + 31) / 32), nseg = (int)bwd_segments(a.L);
+    const int cblocks = (int)((a.D / VEC + 31) / 32), nseg = (int)bwd_segments(a.L);
     const unsigned grid = (unsigned)(a.batch * nseg * cblocks);
 #define FN(IO, G_, W_) conv1d_bwd_kernel<IO, G_, W_><<<grid, kBwdWarps * 32, 0, s>>>(a, cblocks, nseg)
     CONV1D_DISPATCH(FN);

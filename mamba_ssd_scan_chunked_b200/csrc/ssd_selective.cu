@@ -275,40 +275,89 @@ selective_chunks_kernel(const SelectiveArgs a, int nch, float* __restrict__ wsta
     }
 }
 
-// One token: K lanes hold a channel's states, 4 neighbouring ones each (8 with
-// more than 128 states, in two rounds of 4).
-template <typename StateT, typename IoT, typename YT>
+// One token: a stream of the states, each read and written once with 16-byte
+// vectors.  K lanes cover a channel's states (R rounds of a vector each); a thread
+// takes NB sequences of the batch, whose loads are all in flight before the first
+// is used, so that A and the channel's parameters are fetched once for NB states.
+template <typename StateT, typename IoT, typename YT, int R, int NB>
 __global__ void __launch_bounds__(128)
-selective_update_kernel(const SelectiveArgs a, int K, int per_block) {
-    const int lane = threadIdx.x % K, slot = threadIdx.x / K;
-    const int64_t bd = (int64_t)blockIdx.x * per_block + slot, all = a.batch * a.D;
-    const bool live = bd < all;               // every lane takes part in the sums
-    const int64_t b = live ? bd / a.D : 0, d = live ? bd % a.D : 0;
-    const int64_t g = d / (a.D / a.G);
-    const float dt = softplus_f32(to_f32(((const IoT*)a.dt_raw)[b * a.D + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f));
-    const float x = to_f32(((const IoT*)a.x)[b * a.D + d]);
-    float y = 0.f;
-    for (int n = lane * 4; n < a.N; n += K * 4) {
-        const float4 A = *(const float4*)(a.A + d * a.N + n);
-        const float Av[4] = {A.x, A.y, A.z, A.w};
-        StateT* hp = (StateT*)a.final_state + (b * a.D + d) * a.N + n;
-        const IoT* Bp = (const IoT*)a.B + (b * a.G + g) * a.N + n;
-        const IoT* Cp = (const IoT*)a.C + (b * a.G + g) * a.N + n;
+selective_update_kernel(const SelectiveArgs a, int K, int cblocks) {
+    constexpr int VS = Vec16<StateT>::N;
+    const int lane = threadIdx.x % K, slot = threadIdx.x / K, per_block = 128 / K;
+    const int64_t d = (int64_t)(blockIdx.x % (unsigned)cblocks) * per_block + slot;
+    const int64_t b0 = (int64_t)(blockIdx.x / (unsigned)cblocks) * NB;
+    const bool cok = d < a.D;                  // every lane takes part in the sums
+    const int64_t g = cok ? d / (a.D / a.G) : 0;
+    uint4 hr[NB][R];
+    float x[NB], dt[NB], z[NB], Bv[NB][R][VS], Cv[NB][R][VS];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const float h = fmaf(exp2_approx(dt * (Av[s] * kLog2e)), to_f32(hp[s]), dt * x * to_f32(Bp[s]));
-            y = fmaf(to_f32(Cp[s]), h, y);
-            if (live) hp[s] = from_f32<StateT>(h);
+    for (int u = 0; u < NB; ++u) {
+        const int64_t b = b0 + u;
+        const bool live = cok && b < a.batch;
+        x[u] = dt[u] = z[u] = 0.f;
+        if (live) {
+            x[u] = to_f32(((const IoT*)a.x)[b * a.D + d]);
+            dt[u] = to_f32(((const IoT*)a.dt_raw)[b * a.D + d]);
+            if (a.z) z[u] = to_f32(((const IoT*)a.z)[b * a.zs + d]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int n = (lane + r * K) * VS;
+#pragma unroll
+            for (int s = 0; s < VS; ++s) Bv[u][r][s] = Cv[u][r][s] = 0.f;
+            hr[u][r] = make_uint4(0, 0, 0, 0);
+            if (live && n < a.N) {
+                hr[u][r] = __ldcs((const uint4*)((const StateT*)a.final_state + (b * a.D + d) * a.N + n));
+                const IoT* pb = (const IoT*)a.B + (b * a.G + g) * a.N + n;
+                const IoT* pc = (const IoT*)a.C + (b * a.G + g) * a.N + n;
+#pragma unroll
+                for (int s = 0; s < VS; s += 4) {
+                    load4(pb + s, Bv[u][r] + s);
+                    load4(pc + s, Cv[u][r] + s);
+                }
+            }
         }
     }
-    for (int o = 1; o < K; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (live && lane == 0) {
-        y = fmaf(a.Dv ? a.Dv[d] : 0.f, x, y);
-        if (a.z) {
-            const float z = to_f32(((const IoT*)a.z)[b * a.zs + d]);
-            y *= z * sigmoid_f32(z);
+    float A2[R][VS];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = (lane + r * K) * VS;
+#pragma unroll
+        for (int s = 0; s < VS; ++s) A2[r][s] = 0.f;
+        if (cok && n < a.N)
+#pragma unroll
+            for (int s = 0; s < VS; s += 4) {
+                Vec16<float>::load(a.A + d * a.N + n + s, A2[r] + s);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) A2[r][s + q] *= kLog2e;
+            }
+    }
+    const float bias = cok && a.dt_bias ? a.dt_bias[d] : 0.f, Dv = cok && a.Dv ? a.Dv[d] : 0.f;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+        const int64_t b = b0 + u;
+        const bool live = cok && b < a.batch;
+        const float dtv = f2_get(softplus2(dt[u] + bias, 0.f)).x, dx = dtv * x[u];
+        float y = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int n = (lane + r * K) * VS;
+            float h[VS];
+            Vec16<StateT>::unpack(hr[u][r], h);
+#pragma unroll
+            for (int s = 0; s < VS; ++s) {
+                h[s] = fmaf(exp2_approx(dtv * A2[r][s]), h[s], dx * Bv[u][r][s]);
+                y = fmaf(Cv[u][r][s], h[s], y);
+            }
+            if (live && n < a.N)
+                __stcs((uint4*)((StateT*)a.final_state + (b * a.D + d) * a.N + n), Vec16<StateT>::pack(h));
         }
-        ((YT*)a.y)[b * a.D + d] = from_f32<YT>(y);
+        for (int o = 1; o < K; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (live && lane == 0) {
+            y = fmaf(Dv, x[u], y);
+            if (a.z) y *= z[u] * sigmoid_f32(z[u]);
+            ((YT*)a.y)[b * a.D + d] = from_f32<YT>(y);
+        }
     }
 }
 
@@ -394,14 +443,29 @@ cudaError_t launch_selective_fwd(const SelectiveArgs& a, cudaStream_t s) {
     return a.y_bf16 ? launch_fwd_s<float, bf16>(a, s) : launch_fwd_s<float, float>(a, s);
 }
 
+template <typename StateT, typename IoT, typename YT, int R>
+static void launch_update_r(const SelectiveArgs& a, int K, cudaStream_t s) {
+    const int cblocks = (int)((a.D + 128 / K - 1) / (128 / K));
+    // four sequences a thread once that still leaves 1024 threads an SM
+    const int64_t quads = (a.batch + 3) / 4 * cblocks;
+    if (R == 1 && quads >= 148 * 8)
+        selective_update_kernel<StateT, IoT, YT, R, 4><<<(unsigned)quads, 128, 0, s>>>(a, K, cblocks);
+    else
+        selective_update_kernel<StateT, IoT, YT, R, 1><<<(unsigned)(a.batch * cblocks), 128, 0, s>>>(a, K, cblocks);
+}
+
 template <typename StateT, typename IoT>
 static void launch_update_t(const SelectiveArgs& a, cudaStream_t s) {
+    constexpr int VS = Vec16<StateT>::N;
     int K = 1;
-    while (K < 32 && K * 4 < a.N) K *= 2;
-    const int per = 128 / K;
-    const unsigned grid = (unsigned)((a.batch * a.D + per - 1) / per);
-    if (a.y_bf16) selective_update_kernel<StateT, IoT, bf16><<<grid, 128, 0, s>>>(a, K, per);
-    else selective_update_kernel<StateT, IoT, float><<<grid, 128, 0, s>>>(a, K, per);
+    while (K < 32 && K * VS < a.N) K *= 2;
+    if (K * VS < a.N) {
+        if (a.y_bf16) launch_update_r<StateT, IoT, bf16, 2>(a, K, s);
+        else launch_update_r<StateT, IoT, float, 2>(a, K, s);
+    } else {
+        if (a.y_bf16) launch_update_r<StateT, IoT, bf16, 1>(a, K, s);
+        else launch_update_r<StateT, IoT, float, 1>(a, K, s);
+    }
 }
 
 cudaError_t launch_selective_update(const SelectiveArgs& a, cudaStream_t s) {

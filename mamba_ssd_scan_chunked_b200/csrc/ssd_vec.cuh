@@ -17,15 +17,18 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
     Vec16<float>::store(p, v);
     Vec16<float>::store(p + 4, v + 4);
 }
-// the same of an array whose dtype is known at run time only
-__device__ __forceinline__ void load8_dyn(const void* p, bool is_bf16, int64_t i, float* v) {
-    if (is_bf16) load8((const bf16*)p + i, v);
-    else load8((const float*)p + i, v);
+// 4 consecutive elements (aligned to their size) to and from fp32.
+__device__ __forceinline__ void load4(const bf16* p, float* v) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.y << 16); v[3] = __uint_as_float(r.y & 0xffff0000u);
 }
-__device__ __forceinline__ void store8_dyn(void* p, bool is_bf16, int64_t i, const float* v) {
-    if (is_bf16) store8((bf16*)p + i, v);
-    else store8((float*)p + i, v);
+__device__ __forceinline__ void load4(const float* p, float* v) { Vec16<float>::load(p, v); }
+__device__ __forceinline__ void store4(bf16* p, const float* v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+__device__ __forceinline__ void store4(float* p, const float* v) { Vec16<float>::store(p, v); }
 
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -63,6 +63,8 @@ def test_conv1d_fwd(b, L, split, W, io, y, state, init, bias, act, pad, extra):
     (7, (1032, 64, 64), 4, B, B, B, True, True, 40),
     (2, (16, 8), 3, B, F, F, False, False, 8),
     (1, (8,), 2, F, B, F, True, True, 0),
+    (801, (1032, 64, 64), 4, B, B, B, True, True, 8),                   # four sequences a thread, one left over
+    (650, (1160,), 3, F, F, F, True, True, 0),
 ])
 def test_conv1d_update_is_the_forward_token_by_token(b, split, W, io, y, state, bias, act, extra):
     D, L = sum(split), 6

@@ -92,6 +92,8 @@ def test_strong_and_vanishing_decays():
     (2, 24, 128, 1, F, F, F, True, True, 8),
     (1, 8, 200, 1, F, F, F, True, True, 0),
     (9, 40, 8, 1, B, B, F, True, True, 0),
+    (531, 264, 16, 1, B, B, F, True, True, 8),                          # four sequences a thread, three left over
+    (302, 272, 64, 2, F, F, F, True, True, 0),
 ])
 def test_selective_state_update_is_the_scan_token_by_token(b, D, N, G, io, y, state, gate, skip, extra):
     L = 5
@@ -107,8 +109,9 @@ def test_selective_state_update_is_the_scan_token_by_token(b, D, N, G, io, y, st
     check("state", st, fref)
 
 
-def test_selective_state_update_bf16_state_rounds_once():
-    c = case(4, None, 40, 16, 1, B, B, True, True, True, 11)
+@pytest.mark.parametrize("b,D,N", [(4, 40, 16), (3, 24, 256), (600, 264, 8)])
+def test_selective_state_update_bf16_state_rounds_once(b, D, N):
+    c = case(b, None, D, N, 1, B, B, True, True, True, 11)
     f = {k: f64(v) for k, v in c.items()}
     d = on_gpu(c)
     h, y = O.selective_step(f["init"], f["x"], f["dt_raw"], f["dt_bias"], f["A"], f["B"], f["C"], f["D"], f["z"])
