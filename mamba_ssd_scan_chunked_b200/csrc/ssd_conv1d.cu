@@ -7,8 +7,6 @@
 // Every kernel is a stream bound by HBM: a thread owns a few neighbouring
 // channels, walks over a run of tokens with the last W - 1 inputs in registers,
 // and so reads each input once (and W - 1 more per run).
-#include <type_traits>
-
 #include "ssd_internal.h"
 #include "ssd_vec.cuh"
 
@@ -46,21 +44,6 @@ __device__ __forceinline__ int split_of(const Conv1dArgs& a, int64_t c, int64_t*
     *ld = a.part[2]; *at = c - a.part[1];
     return 2;
 }
-
-// VEC channels of a token as they lie in memory (all loads of a round in flight
-// before the first is used)
-template <typename T> struct Raw4 {
-    typename std::conditional<sizeof(T) * VEC == 16, uint4, uint2>::type r;
-    __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const decltype(r)*>(p); }
-    __device__ __forceinline__ void get(f32x2 (&v)[VEC / 2]) const {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-            if constexpr (sizeof(T) == 2) v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-            else v[i] = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-        }
-    }
-};
 
 // the W - 1 inputs before token t0 of a sequence that starts at token p: kept
 // inputs where they lie before p (t0 < p: as of token p)
@@ -156,7 +139,7 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
     load_ring<IoT, W>(a, b, c, t0, p, ring);
     auto token = [&](int t, int u) {
         float out[VEC];
-        next[u].get(ring[u]);
+        next[u].get2(ring[u]);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             f32x2 v = bias[i];
@@ -317,8 +300,8 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
         // token u of a round adds its dv to the gradients (mine: to dw and db too)
         auto token = [&](int u, const Raw4<IoT>& xr, const Raw4<IoT>& yr, bool mine) {
             f32x2 dv[H];
-            xr.get(ring[u]);
-            yr.get(dv);
+            xr.get2(ring[u]);
+            yr.get2(dv);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 if (a.silu) {

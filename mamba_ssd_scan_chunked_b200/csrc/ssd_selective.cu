@@ -276,47 +276,55 @@ selective_chunks_kernel(const SelectiveArgs a, int nch, float* __restrict__ wsta
 }
 
 // One token: a stream of the states, each read and written once with 16-byte
-// vectors.  K lanes cover a channel's states (R rounds of a vector each); a thread
-// takes NB sequences of the batch, whose loads are all in flight before the first
-// is used, so that A and the channel's parameters are fetched once for NB states.
+// vectors.  K lanes cover a channel's states (R rounds of a vector each) for NB <= K
+// sequences of the batch, whose loads are all in flight before the first is used:
+// A is fetched once for NB states.  Of a channel's scalars lane u of the K takes
+// sequence u's: it loads x, dt_raw and z, forms dt and the gate, passes dt and dt x
+// to the others and stores sequence u's y.
 template <typename StateT, typename IoT, typename YT, int R, int NB>
 __global__ void __launch_bounds__(128)
-selective_update_kernel(const SelectiveArgs a, int K, int cblocks) {
+selective_update_kernel(const SelectiveArgs a, int K, int cblocks, int Dg) {
     constexpr int VS = Vec16<StateT>::N;
-    const int lane = threadIdx.x % K, slot = threadIdx.x / K, per_block = 128 / K;
-    const int64_t d = (int64_t)(blockIdx.x % (unsigned)cblocks) * per_block + slot;
-    const int64_t b0 = (int64_t)(blockIdx.x / (unsigned)cblocks) * NB;
-    const bool cok = d < a.D;                  // every lane takes part in the sums
-    const int64_t g = cok ? d / (a.D / a.G) : 0;
+    const int lane = threadIdx.x % K, slot = threadIdx.x / K;
+    const int d = (int)(blockIdx.x % (unsigned)cblocks) * (128 / K) + slot;
+    const int b0 = (int)(blockIdx.x / (unsigned)cblocks) * NB;
+    const int nb = d >= a.D ? 0 : a.batch - b0 < NB ? (int)(a.batch - b0) : NB;   // every lane takes part in the sums
+    const int N = (int)a.N;
+    StateT* hp = (StateT*)a.final_state + (b0 * a.D + d) * N;
+    const IoT* pb = (const IoT*)a.B + ((int64_t)b0 * a.G + d / Dg) * N;
+    const IoT* pc = (const IoT*)a.C + ((int64_t)b0 * a.G + d / Dg) * N;
+    const int64_t hstep = a.D * N, bstep = a.G * N;
     uint4 hr[NB][R];
-    float x[NB], dt[NB], z[NB], Bv[NB][R][VS], Cv[NB][R][VS];
+    Raw4<IoT> Br[NB][R][VS / 4], Cr[NB][R][VS / 4];
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
-        const int64_t b = b0 + u;
-        const bool live = cok && b < a.batch;
-        x[u] = dt[u] = z[u] = 0.f;
-        if (live) {
-            x[u] = to_f32(((const IoT*)a.x)[b * a.D + d]);
-            dt[u] = to_f32(((const IoT*)a.dt_raw)[b * a.D + d]);
-            if (a.z) z[u] = to_f32(((const IoT*)a.z)[b * a.zs + d]);
-        }
+    for (int u = 0; u < NB; ++u)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int n = (lane + r * K) * VS;
-#pragma unroll
-            for (int s = 0; s < VS; ++s) Bv[u][r][s] = Cv[u][r][s] = 0.f;
             hr[u][r] = make_uint4(0, 0, 0, 0);
-            if (live && n < a.N) {
-                hr[u][r] = __ldcs((const uint4*)((const StateT*)a.final_state + (b * a.D + d) * a.N + n));
-                const IoT* pb = (const IoT*)a.B + (b * a.G + g) * a.N + n;
-                const IoT* pc = (const IoT*)a.C + (b * a.G + g) * a.N + n;
 #pragma unroll
-                for (int s = 0; s < VS; s += 4) {
-                    load4(pb + s, Bv[u][r] + s);
-                    load4(pc + s, Cv[u][r] + s);
+            for (int q = 0; q < VS / 4; ++q) {
+                Br[u][r][q].zero();
+                Cr[u][r][q].zero();
+            }
+            if (u < nb && n < N) {
+                hr[u][r] = __ldcs((const uint4*)(hp + u * hstep + n));
+#pragma unroll
+                for (int q = 0; q < VS / 4; ++q) {
+                    Br[u][r][q].load(pb + u * bstep + n + 4 * q);
+                    Cr[u][r][q].load(pc + u * bstep + n + 4 * q);
                 }
             }
         }
+    const int own = lane % NB;
+    const int64_t at = (int64_t)(b0 + own) * a.D + d;
+    float x = 0.f, raw = 0.f, z = 0.f, bias = 0.f, Dv = 0.f;
+    if (own < nb) {
+        x = to_f32(((const IoT*)a.x)[at]);
+        raw = to_f32(((const IoT*)a.dt_raw)[at]);
+        if (a.z) z = to_f32(((const IoT*)a.z)[(b0 + own) * a.zs + d]);
+        if (a.dt_bias) bias = a.dt_bias[d];
+        if (a.Dv) Dv = a.Dv[d];
     }
     float A2[R][VS];
 #pragma unroll
@@ -324,40 +332,45 @@ selective_update_kernel(const SelectiveArgs a, int K, int cblocks) {
         const int n = (lane + r * K) * VS;
 #pragma unroll
         for (int s = 0; s < VS; ++s) A2[r][s] = 0.f;
-        if (cok && n < a.N)
+        if (nb > 0 && n < N)
 #pragma unroll
             for (int s = 0; s < VS; s += 4) {
-                Vec16<float>::load(a.A + d * a.N + n + s, A2[r] + s);
+                Vec16<float>::load(a.A + (int64_t)d * N + n + s, A2[r] + s);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) A2[r][s + q] *= kLog2e;
             }
     }
-    const float bias = cok && a.dt_bias ? a.dt_bias[d] : 0.f, Dv = cok && a.Dv ? a.Dv[d] : 0.f;
+    const float dt = f2_get(softplus2(raw + bias, raw + bias)).x, dx = dt * x;
+    float mine = 0.f;
 #pragma unroll
     for (int u = 0; u < NB; ++u) {
-        const int64_t b = b0 + u;
-        const bool live = cok && b < a.batch;
-        const float dtv = f2_get(softplus2(dt[u] + bias, 0.f)).x, dx = dtv * x[u];
+        const int from = (int)(threadIdx.x & 31) - lane + u;          // the lane of this channel that has sequence u
+        const float dtu = __shfl_sync(0xffffffffu, dt, from), dxu = __shfl_sync(0xffffffffu, dx, from);
         float y = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int n = (lane + r * K) * VS;
-            float h[VS];
+            float h[VS], B[VS], C[VS];
             Vec16<StateT>::unpack(hr[u][r], h);
 #pragma unroll
-            for (int s = 0; s < VS; ++s) {
-                h[s] = fmaf(exp2_approx(dtv * A2[r][s]), h[s], dx * Bv[u][r][s]);
-                y = fmaf(Cv[u][r][s], h[s], y);
+            for (int q = 0; q < VS / 4; ++q) {
+                Br[u][r][q].get(B + 4 * q);
+                Cr[u][r][q].get(C + 4 * q);
             }
-            if (live && n < a.N)
-                __stcs((uint4*)((StateT*)a.final_state + (b * a.D + d) * a.N + n), Vec16<StateT>::pack(h));
+#pragma unroll
+            for (int s = 0; s < VS; ++s) {
+                h[s] = fmaf(exp2_approx(dtu * A2[r][s]), h[s], dxu * B[s]);
+                y = fmaf(C[s], h[s], y);
+            }
+            if (u < nb && n < N) __stcs((uint4*)(hp + u * hstep + n), Vec16<StateT>::pack(h));
         }
         for (int o = 1; o < K; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (live && lane == 0) {
-            y = fmaf(Dv, x[u], y);
-            if (a.z) y *= z[u] * sigmoid_f32(z[u]);
-            ((YT*)a.y)[b * a.D + d] = from_f32<YT>(y);
-        }
+        if (own == u) mine = y;
+    }
+    if (lane < nb) {
+        mine = fmaf(Dv, x, mine);
+        if (a.z) mine *= z * sigmoid_f32(z);
+        ((YT*)a.y)[at] = from_f32<YT>(mine);
     }
 }
 
@@ -445,13 +458,15 @@ cudaError_t launch_selective_fwd(const SelectiveArgs& a, cudaStream_t s) {
 
 template <typename StateT, typename IoT, typename YT, int R>
 static void launch_update_r(const SelectiveArgs& a, int K, cudaStream_t s) {
-    const int cblocks = (int)((a.D + 128 / K - 1) / (128 / K));
-    // four sequences a thread once that still leaves 1024 threads an SM
-    const int64_t quads = (a.batch + 3) / 4 * cblocks;
-    if (R == 1 && quads >= 148 * 8)
-        selective_update_kernel<StateT, IoT, YT, R, 4><<<(unsigned)quads, 128, 0, s>>>(a, K, cblocks);
+    const int cblocks = (int)((a.D + 128 / K - 1) / (128 / K)), Dg = (int)(a.D / a.G);
+    // as many sequences a thread as lanes, up to 4, once that still leaves 1024 threads an SM
+    const int64_t quads = (a.batch + 3) / 4 * cblocks, twos = (a.batch + 1) / 2 * cblocks;
+    if (R == 1 && K >= 4 && quads >= 148 * 8)
+        selective_update_kernel<StateT, IoT, YT, R, R == 1 ? 4 : 1><<<(unsigned)quads, 128, 0, s>>>(a, K, cblocks, Dg);
+    else if (R == 1 && K >= 2 && twos >= 148 * 8)
+        selective_update_kernel<StateT, IoT, YT, R, R == 1 ? 2 : 1><<<(unsigned)twos, 128, 0, s>>>(a, K, cblocks, Dg);
     else
-        selective_update_kernel<StateT, IoT, YT, R, 1><<<(unsigned)(a.batch * cblocks), 128, 0, s>>>(a, K, cblocks);
+        selective_update_kernel<StateT, IoT, YT, R, 1><<<(unsigned)(a.batch * cblocks), 128, 0, s>>>(a, K, cblocks, Dg);
 }
 
 template <typename StateT, typename IoT>

@@ -2,6 +2,8 @@
 // approximations of the special functions, pairs of fp32 operations.
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_common.cuh"
 
 namespace ssd {
@@ -95,6 +97,27 @@ template <> struct Raw8<float> {
     __device__ __forceinline__ void get(float* v) const {
         Vec16<float>::unpack(r[0], v);
         Vec16<float>::unpack(r[1], v + 4);
+    }
+};
+
+// the same for 4 elements; get2 gives them as pairs
+template <typename T> struct Raw4 {
+    typename std::conditional<sizeof(T) == 4, uint4, uint2>::type r;
+    __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const decltype(r)*>(p); }
+    __device__ __forceinline__ void zero() { r = decltype(r){}; }
+    __device__ __forceinline__ void get(float* v) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+            else v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    }
+    __device__ __forceinline__ void get2(f32x2 (&v)[2]) const {
+        float f[4];
+        get(f);
+        v[0] = f2_pack(f[0], f[1]);
+        v[1] = f2_pack(f[2], f[3]);
     }
 };
 
