@@ -111,6 +111,8 @@ _VP = ctypes.c_void_p
 def lib():
     """The loaded libssd.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -330,60 +332,55 @@ def ssd_debug_inject(faults: int) -> int:
 
 def ssd_conv1d_fwd(desc, x, weight, bias, init_state, pad_left, y0, y1, y2, final_state, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    ptrs = (x, weight, bias, init_state, pad_left, y0, y1, y2, final_state, stream)
-    return lib().ssd_conv1d_fwd(ctypes.byref(desc), *(p or None for p in ptrs))
+    return lib().ssd_conv1d_fwd(desc, x, weight, bias, init_state, pad_left, y0, y1, y2, final_state, stream)
 
 
 def ssd_conv1d_update(desc, state, x, weight, bias, y0, y1, y2, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    return lib().ssd_conv1d_update(ctypes.byref(desc), *(p or None for p in (state, x, weight, bias, y0, y1, y2, stream)))
+    return lib().ssd_conv1d_update(desc, state, x, weight, bias, y0, y1, y2, stream)
 
 
 def ssd_conv1d_bwd(desc, x, weight, bias, init_state, dy0, dy1, dy2, dfinal_state, dx, dweight, dbias, dinit_state,
                    workspace, workspace_bytes, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    ptrs = (x, weight, bias, init_state, dy0, dy1, dy2, dfinal_state, dx, dweight, dbias, dinit_state, workspace)
-    return lib().ssd_conv1d_bwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes), stream or None)
+    return lib().ssd_conv1d_bwd(desc, x, weight, bias, init_state, dy0, dy1, dy2, dfinal_state, dx, dweight, dbias,
+                                dinit_state, workspace, workspace_bytes, stream)
 
 
 def ssd_selective_scan_fwd(desc, x, dt_raw, dt_bias, A, B, C, D, z, init_state, pad_left, y, final_state, workspace,
                            workspace_bytes, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    ptrs = (x, dt_raw, dt_bias, A, B, C, D, z, init_state, pad_left, y, final_state, workspace)
-    return lib().ssd_selective_scan_fwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes),
-                                        stream or None)
+    return lib().ssd_selective_scan_fwd(desc, x, dt_raw, dt_bias, A, B, C, D, z, init_state, pad_left, y, final_state,
+                                        workspace, workspace_bytes, stream)
 
 
 def ssd_selective_state_update(desc, state, x, dt_raw, dt_bias, A, B, C, D, z, y, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    ptrs = (state, x, dt_raw, dt_bias, A, B, C, D, z, y, stream)
-    return lib().ssd_selective_state_update(ctypes.byref(desc), *(p or None for p in ptrs))
+    return lib().ssd_selective_state_update(desc, state, x, dt_raw, dt_bias, A, B, C, D, z, y, stream)
 
 
 def ssd_selective_scan_bwd(desc, x, dt_raw, dt_bias, A, B, C, D, z, init_state, dy, dfinal_state, dx, ddt_raw,
                            ddt_bias, dA, dB, dC, dD, dz, dinit_state, workspace, workspace_bytes, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    ptrs = (x, dt_raw, dt_bias, A, B, C, D, z, init_state, dy, dfinal_state, dx, ddt_raw, ddt_bias, dA, dB, dC, dD,
-            dz, dinit_state, workspace)
-    return lib().ssd_selective_scan_bwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes),
-                                        stream or None)
+    return lib().ssd_selective_scan_bwd(desc, x, dt_raw, dt_bias, A, B, C, D, z, init_state, dy, dfinal_state, dx,
+                                        ddt_raw, ddt_bias, dA, dB, dC, dD, dz, dinit_state, workspace, workspace_bytes,
+                                        stream)
 
 
 def ssd_group_norm_fwd(desc, x, z, weight, bias, y, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    return lib().ssd_group_norm_fwd(ctypes.byref(desc), *(p or None for p in (x, z, weight, bias, y, stream)))
+    return lib().ssd_group_norm_fwd(desc, x, z, weight, bias, y, stream)
 
 
 def ssd_group_norm_bwd(desc, x, z, weight, bias, dy, dx, dz, dweight, dbias, workspace, workspace_bytes, stream) -> int:
     """Raw call; returns the status code (0 = enqueued)."""
-    ptrs = (x, z, weight, bias, dy, dx, dz, dweight, dbias, workspace)
-    return lib().ssd_group_norm_bwd(ctypes.byref(desc), *(p or None for p in ptrs), int(workspace_bytes),
-                                    stream or None)
+    return lib().ssd_group_norm_bwd(desc, x, z, weight, bias, dy, dx, dz, dweight, dbias, workspace, workspace_bytes,
+                                    stream)
 
 
 def _size_of(name, desc) -> int:
     n = ctypes.c_size_t(0)
-    st = getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(n))
+    st = getattr(lib(), name)(desc, n)
     if st:
         raise SsdError(st, name)
     return n.value
@@ -423,7 +420,7 @@ def _torch_dtype(code: int):
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else t.data_ptr()
 
 
 def _stream(stream) -> int:
@@ -727,95 +724,101 @@ def state_update_mimo(state, x, dt_raw, dt_bias, A, B, C, D, *, y=None, y_dtype=
 # --------------------------------------------------------------------------
 # the operators around the scan
 # --------------------------------------------------------------------------
+# A token's calls take a few microseconds on the device, so these wrappers read
+# each property of a tensor once.
+def _code(dtype) -> int:
+    c = _CODES.get(dtype)
+    if c is None:
+        c = _CODES[dtype] = _dtype_code(dtype)
+    return c
+
+
+_CODES = {}
+
+
+def _check(t, shape, name, dtype=None):
+    """As ``_expect``."""
+    if t is not None and (t.shape != shape or (dtype is not None and t.dtype != dtype)):
+        _expect(t, shape, name, dtype)
+
+
 def _row_stride(t, name, lead, width, dtype):
     """Elements from a row of ``t`` (shape ``lead + (width,)``, possibly columns cut out of wider
     rows) to the next one; the rows follow each other at one distance."""
-    _expect(t, tuple(lead) + (width,), name, dtype)
-    if t.numel() == 0:
+    _check(t, lead + (width,), name, dtype)
+    if t.is_contiguous():
         return width
-    if t.stride(-1) != 1 and width > 1:
+    strides = t.stride()
+    if strides[-1] != 1 and width > 1:
         raise ValueError(f"{name}: the channels have to be neighbours in memory")
     stride, rows = None, 1
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, st in zip(reversed(lead), reversed(strides[:-1])):
         if n != 1:
             if stride is None:
                 stride = st
             elif st != stride * rows:
-                raise ValueError(f"{name}: rows at one distance expected, strides {t.stride()}")
+                raise ValueError(f"{name}: rows at one distance expected, strides {strides}")
         rows *= n
     if stride is None:
         return width
     if stride < width:
-        raise ValueError(f"{name}: overlapping rows, strides {t.stride()}")
+        raise ValueError(f"{name}: overlapping rows, strides {strides}")
     return stride
 
 
-def _on_one_device(dense, rows=()):
-    """The CUDA device of all the tensors (None passes); the ``dense`` ones have to be contiguous."""
-    device = None
-    for t in (*dense, *rows):
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libssd takes contiguous CUDA tensors")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}: libssd takes them on one device")
+def _one_device(dense, rows=()) -> int:
+    """The index of the CUDA device of all the tensors (None passes); the ``dense`` ones have to be contiguous."""
+    index = None
     for t in dense:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("libssd takes contiguous CUDA tensors")
-    return device
+        if t is not None:
+            i = t.get_device()
+            if i != index:
+                if i < 0:
+                    raise ValueError("libssd takes contiguous CUDA tensors")
+                if index is not None:
+                    raise ValueError(f"tensors on devices {index} and {i}: libssd takes them on one device")
+                index = i
+            if not t.is_contiguous():
+                raise ValueError("libssd takes contiguous CUDA tensors")
+    for t in rows:
+        if t is not None and t.get_device() != index:
+            if t.get_device() < 0:
+                raise ValueError("libssd takes contiguous CUDA tensors")
+            if index is not None:
+                raise ValueError(f"tensors on devices {index} and {t.get_device()}: libssd takes them on one device")
+            index = t.get_device()
+    return index
 
 
-class _LaunchOn:
-    """Makes ``device`` the current one and ``stream`` (None: the device's current stream) the stream
-    that outputs and workspaces are allocated for; gives the stream's handle."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.contexts = []
-        if device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-            return
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream.device != device:
-            raise ValueError(f"stream on {stream.device}, tensors on {device}")
-        self.contexts.append(torch.cuda.stream(stream))
-        self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return int(self.handle)
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-
-
-def _workspace(workspace, need, device):
-    """The caller's workspace when it is large enough, else one of this call's own."""
+def _launch_on(index, stream, call):
+    """``call(handle)`` with device ``index`` the current one and ``stream`` (None: the device's current
+    stream) the one that outputs and workspaces are allocated for and the call is enqueued on."""
     import torch
-    if workspace is not None and workspace.numel() * workspace.element_size() >= need:
-        return workspace, workspace.numel() * workspace.element_size()
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(index))   # the handle alone, 3 us less than the object
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    if stream.device.index != index:
+        raise ValueError(f"stream on device {stream.device.index}, tensors on device {index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _workspace(workspace, need, x):
+    """The address and size of the caller's workspace when it is large enough, else of one of this call's
+    own beside x, and the tensor."""
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+        if nbytes >= need:
+            return workspace.data_ptr(), nbytes, workspace
     if need == 0:
-        return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=device), need
-
-
-def _check_workspace(workspace):
-    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
-        raise ValueError("workspace: a contiguous CUDA tensor")
-
-
-def _check_pad(pad_left, batch):
+        return 0, 0, None
     import torch
-    if pad_left is not None:
-        _expect(pad_left, (batch,), "pad_left", torch.int32)
+    workspace = x.new_empty(need, dtype=torch.uint8)
+    return workspace.data_ptr(), need, workspace
 
 
 def _silu_flag(activation) -> int:
@@ -825,7 +828,7 @@ def _silu_flag(activation) -> int:
 
 
 def _split_widths(split, channels):
-    widths = (channels,) if split is None else tuple(int(n) for n in split)
+    widths = (channels,) if split is None else tuple(split)
     if not 1 <= len(widths) <= 3 or min(widths) < 1 or sum(widths) != channels:
         raise ValueError(f"split: {split}, expected one to three widths that add up to {channels} channels")
     return widths
@@ -839,8 +842,19 @@ def _conv_outputs(y, widths, lead, dtype, one):
     if len(y) != len(widths):
         raise ValueError(f"y: {len(y)} tensors, expected {len(widths)}")
     for t, n in zip(y, widths):
-        _expect(t, tuple(lead) + (n,), "y", dtype)
+        _check(t, lead + (n,), "y", dtype)
     return y
+
+
+def _three(tensors):
+    """The addresses of up to three tensors, 0 for those that are not there."""
+    return [t.data_ptr() for t in tensors] + [0] * (3 - len(tensors))
+
+
+def _conv_desc(b, L, D, W, xs, dxs, widths, io, y, state, activation) -> Conv1dDesc:
+    n = len(widths)
+    return Conv1dDesc(b, L, D, W, xs, dxs, widths[1] if n > 1 else 0, widths[2] if n > 2 else 0, _code(io), _code(y),
+                      _code(state), _silu_flag(activation))
 
 
 def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation="silu", pad_left=None, y=None,
@@ -863,24 +877,28 @@ def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation=
     if state_dtype is None:
         state_dtype = (init_state.dtype if init_state is not None else
                        final_state.dtype if final_state is not None else torch.float32)
-    _expect(weight, (D, W), "weight", torch.float32)
-    _expect(bias, (D,), "bias", torch.float32)
-    _expect(init_state, (b, W - 1, D), "init_state", state_dtype)
-    _expect(final_state, (b, W - 1, D), "final_state", state_dtype)
-    _check_pad(pad_left, b)
+    kept = (b, W - 1, D)
+    _check(weight, (D, W), "weight", torch.float32)
+    _check(bias, (D,), "bias", torch.float32)
+    _check(init_state, kept, "init_state", state_dtype)
+    _check(final_state, kept, "final_state", state_dtype)
+    _check(pad_left, (b,), "pad_left", torch.int32)
     out = _conv_outputs(y, widths, (b, L), y_dtype, split is None)
-    desc = Conv1dDesc(b, L, D, W, xs, D, *(widths[1:] + (0, 0))[:2], _dtype_code(x.dtype), _dtype_code(y_dtype),
-                      _dtype_code(state_dtype), _silu_flag(activation))
-    device = _on_one_device((weight, bias, init_state, pad_left, final_state, *out), (x,))
-    with _LaunchOn(device, stream) as handle:
-        out = [torch.empty((b, L, n), dtype=y_dtype, device=device) if t is None else t for t, n in zip(out, widths)]
-        if final_state is None and want_final_state:
-            final_state = torch.empty((b, W - 1, D), dtype=state_dtype, device=device)
-        st = ssd_conv1d_fwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(init_state), _ptr(pad_left),
-                            *([_ptr(t) for t in out] + [0, 0])[:3], _ptr(final_state), handle)
-    if st:
-        raise SsdError(st, "ssd_conv1d_fwd")
-    return (out[0] if split is None else tuple(out)), final_state
+    desc = _conv_desc(b, L, D, W, xs, D, widths, x.dtype, y_dtype, state_dtype, activation)
+    device = _one_device((weight, bias, init_state, pad_left, final_state, *out), (x,))
+
+    def call(handle):
+        ys = [x.new_empty((b, L, n), dtype=y_dtype) if t is None else t for t, n in zip(out, widths)]
+        final = final_state
+        if final is None and want_final_state:
+            final = x.new_empty(kept, dtype=state_dtype)
+        st = ssd_conv1d_fwd(desc, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(init_state), _ptr(pad_left),
+                            *_three(ys), _ptr(final), handle)
+        if st:
+            raise SsdError(st, "ssd_conv1d_fwd")
+        return (ys[0] if split is None else tuple(ys)), final
+
+    return _launch_on(device, stream, call)
 
 
 def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu", y=None, y_dtype=None, stream=None):
@@ -893,20 +911,21 @@ def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu",
     xs = _row_stride(x, "x", (b,), D, None)
     if y_dtype is None:
         y_dtype = x.dtype if y is None else (y if hasattr(y, "dtype") else y[0]).dtype
-    _expect(weight, (D, W), "weight", torch.float32)
-    _expect(bias, (D,), "bias", torch.float32)
-    _expect(state, (b, W - 1, D), "state")
+    _check(weight, (D, W), "weight", torch.float32)
+    _check(bias, (D,), "bias", torch.float32)
+    _check(state, (b, W - 1, D), "state")
     out = _conv_outputs(y, widths, (b,), y_dtype, split is None)
-    desc = Conv1dDesc(b, 1, D, W, xs, D, *(widths[1:] + (0, 0))[:2], _dtype_code(x.dtype), _dtype_code(y_dtype),
-                      _dtype_code(state.dtype), _silu_flag(activation))
-    device = _on_one_device((state, weight, bias, *out), (x,))
-    with _LaunchOn(device, stream) as handle:
-        out = [torch.empty((b, n), dtype=y_dtype, device=device) if t is None else t for t, n in zip(out, widths)]
-        st = ssd_conv1d_update(desc, _ptr(state), _ptr(x), _ptr(weight), _ptr(bias),
-                               *([_ptr(t) for t in out] + [0, 0])[:3], handle)
-    if st:
-        raise SsdError(st, "ssd_conv1d_update")
-    return out[0] if split is None else tuple(out)
+    desc = _conv_desc(b, 1, D, W, xs, D, widths, x.dtype, y_dtype, state.dtype, activation)
+    device = _one_device((state, weight, bias, *out), (x,))
+
+    def call(handle):
+        ys = [x.new_empty((b, n), dtype=y_dtype) if t is None else t for t, n in zip(out, widths)]
+        st = ssd_conv1d_update(desc, state.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), *_three(ys), handle)
+        if st:
+            raise SsdError(st, "ssd_conv1d_update")
+        return ys[0] if split is None else tuple(ys)
+
+    return _launch_on(device, stream, call)
 
 
 def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activation="silu", dx=None,
@@ -930,49 +949,49 @@ def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activ
     if state_dtype is None:
         src = init_state if init_state is not None else dfinal_state
         state_dtype = src.dtype if src is not None else torch.float32
-    _expect(weight, (D, W), "weight", torch.float32)
-    _expect(bias, (D,), "bias", torch.float32)
-    _expect(init_state, (b, W - 1, D), "init_state", state_dtype)
-    _expect(dfinal_state, (b, W - 1, D), "dfinal_state", state_dtype)
+    kept = (b, W - 1, D)
+    _check(weight, (D, W), "weight", torch.float32)
+    _check(bias, (D,), "bias", torch.float32)
+    _check(init_state, kept, "init_state", state_dtype)
+    _check(dfinal_state, kept, "dfinal_state", state_dtype)
     for t, n in zip(dys, widths):
-        _expect(t, (b, L, n), "dy", x.dtype)
-    desc = Conv1dDesc(b, L, D, W, xs, dxs, *(widths[1:] + (0, 0))[:2], _dtype_code(x.dtype), _dtype_code(grad_dtype),
-                      _dtype_code(state_dtype), _silu_flag(activation))
-    _check_workspace(workspace)
-    device = _on_one_device((weight, bias, init_state, dfinal_state, workspace, *dys), (x, dx))
+        _check(t, (b, L, n), "dy", x.dtype)
+    desc = _conv_desc(b, L, D, W, xs, dxs, widths, x.dtype, grad_dtype, state_dtype, activation)
+    device = _one_device((weight, bias, init_state, dfinal_state, workspace, *dys), (x, dx))
     need = ssd_conv1d_bwd_workspace_size(desc)
-    with _LaunchOn(device, stream) as handle:
-        f32 = {"dtype": torch.float32, "device": device}
-        out = {"dx": torch.empty((b, L, D), dtype=grad_dtype, device=device) if dx is None else dx,
-               "dweight": torch.empty((D, W), **f32), "dbias": torch.empty(D, **f32) if bias is not None else None,
-               "dinit_state": torch.empty((b, W - 1, D), dtype=state_dtype, device=device) if want_dinit else None}
-        workspace, nbytes = _workspace(workspace, need, device)
-        st = ssd_conv1d_bwd(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(init_state),
-                            *([_ptr(t) for t in dys] + [0, 0])[:3], _ptr(dfinal_state), _ptr(out["dx"]),
-                            _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dinit_state"]), _ptr(workspace), nbytes,
-                            handle)
-    if st:
-        raise SsdError(st, "ssd_conv1d_bwd")
-    return out
+
+    def call(handle):
+        f32, empty = torch.float32, x.new_empty
+        out = {"dx": empty((b, L, D), dtype=grad_dtype) if dx is None else dx,
+               "dweight": empty((D, W), dtype=f32),
+               "dbias": empty(D, dtype=f32) if bias is not None else None,
+               "dinit_state": empty(kept, dtype=state_dtype) if want_dinit else None}
+        ws, nbytes, keep = _workspace(workspace, need, x)
+        st = ssd_conv1d_bwd(desc, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(init_state), *_three(dys),
+                            _ptr(dfinal_state), out["dx"].data_ptr(), out["dweight"].data_ptr(), _ptr(out["dbias"]),
+                            _ptr(out["dinit_state"]), ws, nbytes, handle)
+        if st:
+            raise SsdError(st, "ssd_conv1d_bwd")
+        return out
+
+    return _launch_on(device, stream, call)
 
 
-def _selective_desc(x, B, z, lead, y_dtype, state_dtype) -> SelectiveDesc:
-    D, G, N = x.shape[-1], B.shape[-2], B.shape[-1]
-    b, L = (lead[0], 1) if len(lead) == 1 else lead
-    zs = D if z is None else _row_stride(z, "z", lead, D, x.dtype)
-    return SelectiveDesc(b, L, D, N, G, zs, _dtype_code(x.dtype), _dtype_code(y_dtype), _dtype_code(state_dtype))
-
-
-def _check_selective_args(lead, x, dt_raw, dt_bias, A, B, C, D):
+def _selective_args(lead, x, dt_raw, dt_bias, A, B, C, D, z, y_dtype, state_dtype) -> SelectiveDesc:
+    """The arguments that the calls of the selective scan share, checked, as its descriptor."""
     import torch
-    ch, bc = x.shape[-1], tuple(B.shape[-2:])
-    _expect(x, tuple(lead) + (ch,), "x")
-    _expect(dt_raw, tuple(x.shape), "dt_raw", x.dtype)
-    _expect(B, tuple(lead) + bc, "B", x.dtype)
-    _expect(C, tuple(lead) + bc, "C", x.dtype)
-    _expect(A, (ch, bc[1]), "A", torch.float32)
-    _expect(dt_bias, (ch,), "dt_bias", torch.float32)
-    _expect(D, (ch,), "D", torch.float32)
+    f32, ch, dtype = torch.float32, x.shape[-1], x.dtype
+    G, N = B.shape[-2:]
+    bc = lead + (G, N)
+    _check(dt_raw, lead + (ch,), "dt_raw", dtype)
+    _check(B, bc, "B", dtype)
+    _check(C, bc, "C", dtype)
+    _check(A, (ch, N), "A", f32)
+    _check(dt_bias, (ch,), "dt_bias", f32)
+    _check(D, (ch,), "D", f32)
+    zs = ch if z is None else _row_stride(z, "z", lead, ch, dtype)
+    return SelectiveDesc(lead[0], lead[1] if len(lead) > 1 else 1, ch, N, G, zs, _code(dtype), _code(y_dtype),
+                         _code(state_dtype))
 
 
 def selective_scan_fwd(x, dt_raw, dt_bias, A, B, C, D, z=None, init_state=None, *, y=None, final_state=None,
@@ -987,33 +1006,34 @@ def selective_scan_fwd(x, dt_raw, dt_bias, A, B, C, D, z=None, init_state=None, 
     """
     import torch
     b, L, ch = x.shape
-    N = B.shape[-1]
     if y_dtype is None:
         y_dtype = x.dtype if y is None else y.dtype
     if state_dtype is None:
         state_dtype = (init_state.dtype if init_state is not None else
                        final_state.dtype if final_state is not None else torch.float32)
-    _check_selective_args((b, L), x, dt_raw, dt_bias, A, B, C, D)
-    _expect(init_state, (b, ch, N), "init_state", state_dtype)
-    _expect(final_state, (b, ch, N), "final_state", state_dtype)
-    _expect(y, (b, L, ch), "y", y_dtype)
-    _check_pad(pad_left, b)
-    desc = _selective_desc(x, B, z, (b, L), y_dtype, state_dtype)
-    _check_workspace(workspace)
-    device = _on_one_device((x, dt_raw, dt_bias, A, B, C, D, init_state, pad_left, y, final_state, workspace), (z,))
+    desc = _selective_args((b, L), x, dt_raw, dt_bias, A, B, C, D, z, y_dtype, state_dtype)
+    states = (b, ch, B.shape[-1])
+    _check(init_state, states, "init_state", state_dtype)
+    _check(final_state, states, "final_state", state_dtype)
+    _check(y, (b, L, ch), "y", y_dtype)
+    _check(pad_left, (b,), "pad_left", torch.int32)
+    device = _one_device((x, dt_raw, dt_bias, A, B, C, D, init_state, pad_left, y, final_state, workspace), (z,))
     need = ssd_selective_scan_workspace_size(desc)
-    with _LaunchOn(device, stream) as handle:
-        if y is None:
-            y = torch.empty((b, L, ch), dtype=y_dtype, device=device)
-        if final_state is None and want_final_state:
-            final_state = torch.empty((b, ch, N), dtype=state_dtype, device=device)
-        workspace, nbytes = _workspace(workspace, need, device)
-        st = ssd_selective_scan_fwd(desc, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                    _ptr(z), _ptr(init_state), _ptr(pad_left), _ptr(y), _ptr(final_state),
-                                    _ptr(workspace), nbytes, handle)
-    if st:
-        raise SsdError(st, "ssd_selective_scan_fwd")
-    return y, final_state
+
+    def call(handle):
+        out = x.new_empty((b, L, ch), dtype=y_dtype) if y is None else y
+        final = final_state
+        if final is None and want_final_state:
+            final = x.new_empty(states, dtype=state_dtype)
+        ws, nbytes, keep = _workspace(workspace, need, x)
+        st = ssd_selective_scan_fwd(desc, x.data_ptr(), dt_raw.data_ptr(), _ptr(dt_bias), A.data_ptr(), B.data_ptr(),
+                                    C.data_ptr(), _ptr(D), _ptr(z), _ptr(init_state), _ptr(pad_left), out.data_ptr(),
+                                    _ptr(final), ws, nbytes, handle)
+        if st:
+            raise SsdError(st, "ssd_selective_scan_fwd")
+        return out, final
+
+    return _launch_on(device, stream, call)
 
 
 def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=None, y_dtype=None, stream=None):
@@ -1023,19 +1043,21 @@ def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=N
     b, ch = x.shape
     if y_dtype is None:
         y_dtype = x.dtype if y is None else y.dtype
-    _check_selective_args((b,), x, dt_raw, dt_bias, A, B, C, D)
-    _expect(state, (b, ch, B.shape[-1]), "state")
-    _expect(y, (b, ch), "y", y_dtype)
-    desc = _selective_desc(x, B, z, (b,), y_dtype, state.dtype)
-    device = _on_one_device((state, x, dt_raw, dt_bias, A, B, C, D, y), (z,))
-    with _LaunchOn(device, stream) as handle:
-        if y is None:
-            y = torch.empty((b, ch), dtype=y_dtype, device=device)
-        st = ssd_selective_state_update(desc, _ptr(state), _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(A), _ptr(B),
-                                        _ptr(C), _ptr(D), _ptr(z), _ptr(y), handle)
-    if st:
-        raise SsdError(st, "ssd_selective_state_update")
-    return y
+    desc = _selective_args((b,), x, dt_raw, dt_bias, A, B, C, D, z, y_dtype, state.dtype)
+    _check(state, (b, ch, B.shape[-1]), "state")
+    _check(y, (b, ch), "y", y_dtype)
+    device = _one_device((state, x, dt_raw, dt_bias, A, B, C, D, y), (z,))
+
+    def call(handle):
+        out = x.new_empty((b, ch), dtype=y_dtype) if y is None else y
+        st = ssd_selective_state_update(desc, state.data_ptr(), x.data_ptr(), dt_raw.data_ptr(), _ptr(dt_bias),
+                                        A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), out.data_ptr(),
+                                        handle)
+        if st:
+            raise SsdError(st, "ssd_selective_state_update")
+        return out
+
+    return _launch_on(device, stream, call)
 
 
 def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=None, dfinal_state=None, *,
@@ -1049,55 +1071,58 @@ def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=No
     """
     import torch
     b, L, ch = x.shape
-    G, N = B.shape[-2:]
     if grad_dtype is None:
         grad_dtype = x.dtype
     if state_dtype is None:
         src = init_state if init_state is not None else dfinal_state
         state_dtype = src.dtype if src is not None else torch.float32
-    _check_selective_args((b, L), x, dt_raw, dt_bias, A, B, C, D)
-    _expect(dy, (b, L, ch), "dy", x.dtype)
-    _expect(init_state, (b, ch, N), "init_state", state_dtype)
-    _expect(dfinal_state, (b, ch, N), "dfinal_state", state_dtype)
-    desc = _selective_desc(x, B, z, (b, L), grad_dtype, state_dtype)
-    _check_workspace(workspace)
-    device = _on_one_device((x, dt_raw, dt_bias, A, B, C, D, dy, init_state, dfinal_state, workspace), (z,))
+    desc = _selective_args((b, L), x, dt_raw, dt_bias, A, B, C, D, z, grad_dtype, state_dtype)
+    states = (b, ch, B.shape[-1])
+    _check(dy, (b, L, ch), "dy", x.dtype)
+    _check(init_state, states, "init_state", state_dtype)
+    _check(dfinal_state, states, "dfinal_state", state_dtype)
+    device = _one_device((x, dt_raw, dt_bias, A, B, C, D, dy, init_state, dfinal_state, workspace), (z,))
     need = ssd_selective_scan_bwd_workspace_size(desc)
-    with _LaunchOn(device, stream) as handle:
-        gd, f32 = {"dtype": grad_dtype, "device": device}, {"dtype": torch.float32, "device": device}
-        out = {"dx": torch.empty((b, L, ch), **gd), "ddt_raw": torch.empty((b, L, ch), **gd),
-               "dz": torch.empty((b, L, ch), **gd) if z is not None else None,
-               "dB": torch.empty((b, L, G, N), **gd), "dC": torch.empty((b, L, G, N), **gd),
-               "dA": torch.empty((ch, N), **f32), "ddt_bias": torch.empty(ch, **f32) if dt_bias is not None else None,
-               "dD": torch.empty(ch, **f32) if D is not None else None,
-               "dinit_state": torch.empty((b, ch, N), dtype=state_dtype, device=device) if want_dinit else None}
-        workspace, nbytes = _workspace(workspace, need, device)
-        st = ssd_selective_scan_bwd(desc, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                    _ptr(z), _ptr(init_state), _ptr(dy), _ptr(dfinal_state), _ptr(out["dx"]),
-                                    _ptr(out["ddt_raw"]), _ptr(out["ddt_bias"]), _ptr(out["dA"]), _ptr(out["dB"]),
-                                    _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["dinit_state"]),
-                                    _ptr(workspace), nbytes, handle)
-    if st:
-        raise SsdError(st, "ssd_selective_scan_bwd")
-    return out
+
+    def call(handle):
+        f32, empty = torch.float32, x.new_empty
+        out = {"dx": empty((b, L, ch), dtype=grad_dtype),
+               "ddt_raw": empty((b, L, ch), dtype=grad_dtype),
+               "dz": empty((b, L, ch), dtype=grad_dtype) if z is not None else None,
+               "dB": empty(B.shape, dtype=grad_dtype), "dC": empty(B.shape, dtype=grad_dtype),
+               "dA": empty(A.shape, dtype=f32),
+               "ddt_bias": empty(ch, dtype=f32) if dt_bias is not None else None,
+               "dD": empty(ch, dtype=f32) if D is not None else None,
+               "dinit_state": empty(states, dtype=state_dtype) if want_dinit else None}
+        ws, nbytes, keep = _workspace(workspace, need, x)
+        st = ssd_selective_scan_bwd(desc, x.data_ptr(), dt_raw.data_ptr(), _ptr(dt_bias), A.data_ptr(), B.data_ptr(),
+                                    C.data_ptr(), _ptr(D), _ptr(z), _ptr(init_state), dy.data_ptr(),
+                                    _ptr(dfinal_state), out["dx"].data_ptr(), out["ddt_raw"].data_ptr(),
+                                    _ptr(out["ddt_bias"]), out["dA"].data_ptr(), out["dB"].data_ptr(),
+                                    out["dC"].data_ptr(), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["dinit_state"]),
+                                    ws, nbytes, handle)
+        if st:
+            raise SsdError(st, "ssd_selective_scan_bwd")
+        return out
+
+    return _launch_on(device, stream, call)
 
 
 def _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype) -> GroupNormDesc:
     import torch
-    C, lead = x.shape[-1], tuple(x.shape[:-1])
-    rows = 1
+    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    _check(weight, (C,), "weight", torch.float32)
+    _check(bias, (C,), "bias", torch.float32)
+    act, zs, rows = _silu_flag(activation), C, 1
     for n in lead:
         rows *= n
-    _expect(weight, (C,), "weight", torch.float32)
-    _expect(bias, (C,), "bias", torch.float32)
-    act, zs = _silu_flag(activation), C
     if z is not None:
         if act:
             raise ValueError("activation: the gate z has its own SiLU")
         zs = _row_stride(z, "z", lead, C, io_dtype)
         act = SSD_NORM_GATE_BEFORE if gate_first else SSD_NORM_GATE_AFTER
-    return GroupNormDesc(rows, C, int(ngroups), zs, float(eps), _dtype_code(x.dtype), _dtype_code(io_dtype),
-                         _dtype_code(y_dtype), int(bool(center)), act)
+    return GroupNormDesc(rows, C, ngroups, zs, eps, _code(x.dtype), _code(io_dtype), _code(y_dtype),
+                         1 if center else 0, act)
 
 
 def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, center=False, gate_first=True,
@@ -1110,19 +1135,21 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, ce
     (``y_dtype``, default z's dtype, else x's).
     """
     import torch
+    io_dtype = z.dtype if z is not None else x.dtype
     if y_dtype is None:
-        y_dtype = y.dtype if y is not None else z.dtype if z is not None else x.dtype
-    desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation,
-                      z.dtype if z is not None else x.dtype, y_dtype)
-    _expect(y, tuple(x.shape), "y", y_dtype)
-    device = _on_one_device((x, weight, bias, y), (z,))
-    with _LaunchOn(device, stream) as handle:
-        if y is None:
-            y = torch.empty(x.shape, dtype=y_dtype, device=device)
-        st = ssd_group_norm_fwd(desc, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(y), handle)
-    if st:
-        raise SsdError(st, "ssd_group_norm_fwd")
-    return y
+        y_dtype = y.dtype if y is not None else io_dtype
+    desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype)
+    _check(y, x.shape, "y", y_dtype)
+    device = _one_device((x, weight, bias, y), (z,))
+
+    def call(handle):
+        out = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
+        st = ssd_group_norm_fwd(desc, x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias), out.data_ptr(), handle)
+        if st:
+            raise SsdError(st, "ssd_group_norm_fwd")
+        return out
+
+    return _launch_on(device, stream, call)
 
 
 def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=False, gate_first=True,
@@ -1133,20 +1160,22 @@ def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=F
     if grad_dtype is None:
         grad_dtype = dy.dtype
     desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, dy.dtype, grad_dtype)
-    _expect(dy, tuple(x.shape), "dy")
-    _check_workspace(workspace)
-    device = _on_one_device((x, weight, bias, dy, workspace), (z,))
+    _check(dy, x.shape, "dy")
+    device = _one_device((x, weight, bias, dy, workspace), (z,))
     need = ssd_group_norm_bwd_workspace_size(desc)
-    with _LaunchOn(device, stream) as handle:
-        f32 = {"dtype": torch.float32, "device": device}
-        out = {"dx": torch.empty(x.shape, dtype=grad_dtype, device=device),
-               "dz": torch.empty(x.shape, dtype=grad_dtype, device=device) if z is not None else None,
-               "dweight": torch.empty(x.shape[-1], **f32) if weight is not None else None,
-               "dbias": torch.empty(x.shape[-1], **f32) if bias is not None else None}
-        workspace, nbytes = _workspace(workspace, need, device)
-        st = ssd_group_norm_bwd(desc, _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(out["dx"]),
-                                _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(workspace), nbytes,
-                                handle)
-    if st:
-        raise SsdError(st, "ssd_group_norm_bwd")
-    return out
+
+    def call(handle):
+        f32, empty, C = torch.float32, x.new_empty, x.shape[-1]
+        out = {"dx": empty(x.shape, dtype=grad_dtype),
+               "dz": empty(x.shape, dtype=grad_dtype) if z is not None else None,
+               "dweight": empty(C, dtype=f32) if weight is not None else None,
+               "dbias": empty(C, dtype=f32) if bias is not None else None}
+        ws, nbytes, keep = _workspace(workspace, need, x)
+        st = ssd_group_norm_bwd(desc, x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias), dy.data_ptr(),
+                                out["dx"].data_ptr(), _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), ws,
+                                nbytes, handle)
+        if st:
+            raise SsdError(st, "ssd_group_norm_bwd")
+        return out
+
+    return _launch_on(device, stream, call)

@@ -295,14 +295,27 @@ def test_rows_of_wider_tensors():
 
 def test_tensors_on_several_devices_are_refused():
     class Fake:
-        is_cuda = True
-
         def __init__(self, i):
-            self.device = torch.device("cuda", i)
+            self.i = i
+
+        def get_device(self):
+            return self.i
 
         def is_contiguous(self):
             return True
 
-    assert ssd._on_one_device((Fake(1), None, Fake(1))) == torch.device("cuda", 1)
-    with pytest.raises(ValueError, match="one device"):
-        ssd._on_one_device((Fake(0),), (Fake(1),))
+    assert ssd._one_device((Fake(1), None, Fake(1)), (None, Fake(1))) == 1
+    for dense, rows in (((Fake(0), Fake(1)), ()), ((Fake(0),), (Fake(1),))):
+        with pytest.raises(ValueError, match="one device"):
+            ssd._one_device(dense, rows)
+    for dense, rows in (((Fake(0), Fake(-1)), ()), ((Fake(0),), (Fake(-1),))):
+        with pytest.raises(ValueError, match="CUDA"):
+            ssd._one_device(dense, rows)
+
+
+def test_the_stream_of_another_device_is_refused(monkeypatch):
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream on device 1"):
+        ssd._launch_on(0, Stream(), lambda handle: handle)
