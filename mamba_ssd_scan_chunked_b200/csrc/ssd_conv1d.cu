@@ -477,7 +477,8 @@ cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s) {
 #undef FN
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_column_sum2(a.ws, a.batch * nseg, nw + a.D, a.dw, nw, a.db, s);
+    const ColumnSum sum = {a.ws, a.batch * nseg, nw + a.D, nw + a.D, a.dw, nw, a.db, false};
+    return launch_column_sums(&sum, 1, s);
 }
 
 }  // namespace ssd

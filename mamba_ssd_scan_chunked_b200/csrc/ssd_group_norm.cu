@@ -412,11 +412,12 @@ cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s) {
     NormClass cls;
     const NormShape sh = norm_shape(a.rows, a.C, a.G, true, &cls);
     dispatch_types<NormBwd>(a, sh, cls, s);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!a.dw && !a.db)) return e;
     const int64_t rows = sh.blocks * sh.per_block / a.G;
-    if (e == cudaSuccess && a.dw) e = launch_column_sum(a.ws, rows, a.C, a.C, a.dw, false, s);
-    if (e == cudaSuccess && a.db) e = launch_column_sum(a.ws + rows * a.C, rows, a.C, a.C, a.db, false, s);
-    return e;
+    const ColumnSum sums[] = {{a.ws, rows, a.C, a.dw ? a.C : 0, a.dw, a.C, nullptr, false},
+                              {a.ws + rows * a.C, rows, a.C, a.db ? a.C : 0, a.db, a.C, nullptr, false}};
+    return launch_column_sums(sums, 2, s);
 }
 
 }  // namespace ssd

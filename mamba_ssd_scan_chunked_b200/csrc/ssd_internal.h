@@ -270,13 +270,19 @@ size_t group_norm_bwd_workspace(int64_t rows, int64_t C, int64_t G);
 cudaError_t launch_group_norm_fwd(const GroupNormArgs& a, cudaStream_t s);
 cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s);
 
-// out[c] = sum of column c of part [rows][stride], c < cols, in a fixed order
-// (ssd_column_sum.cu); out is bf16 or fp32
-cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t stride, int64_t cols, void* out, bool out_bf16,
-                              cudaStream_t s);
-// the same into two arrays: columns 0 .. cols1 - 1 to out, the others to out2 (not written when NULL)
-cudaError_t launch_column_sum2(const float* part, int64_t rows, int64_t cols, float* out, int64_t cols1, float* out2,
-                               cudaStream_t s);
+// Column sums (ssd_column_sum.cu): columns 0 .. cols1 - 1 of part [rows][stride] to
+// out, the others up to cols to out2 (neither is written where NULL), in a fixed
+// order; out and out2 are bf16 or fp32.
+struct ColumnSum {
+    const float* part;
+    int64_t rows, stride, cols;
+    void* out;
+    int64_t cols1;
+    void* out2;
+    bool out_bf16;
+};
+constexpr int kMaxColumnSums = 3;
+cudaError_t launch_column_sums(const ColumnSum* sums, int n, cudaStream_t s);
 
 // fault-injection bits set by ssd_debug_inject (read at every launch)
 uint32_t debug_faults();

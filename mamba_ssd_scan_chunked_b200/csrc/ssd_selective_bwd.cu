@@ -51,7 +51,7 @@ struct SbShape {
     size_t off_dt;               // fp32 [b][nch][D] sum of dt
     size_t off_dA;               // fp32 [b][nch][D][N]
     size_t off_par;              // fp32 [b][nch][2][D]: d dt_bias, dD
-    size_t off_dB, off_dC;       // fp32 [split][b][L][G][N]
+    size_t off_dBC;              // fp32 [split][dB, dC][b][L][G][N]
     size_t total;
 };
 
@@ -78,10 +78,8 @@ static SbShape sb_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t 
     l.off_dt = up(l.off_g + st);
     l.off_dA = up(l.off_dt + bn * D * sizeof(float));
     l.off_par = up(l.off_dA + st);
-    l.off_dB = up(l.off_par + bn * 2 * D * sizeof(float));
-    const size_t bc = (size_t)l.split * batch * L * G * N * sizeof(float);
-    l.off_dC = up(l.off_dB + bc);
-    l.total = up(l.off_dC + bc);
+    l.off_dBC = up(l.off_par + bn * 2 * D * sizeof(float));
+    l.total = up(l.off_dBC + (size_t)l.split * 2 * batch * L * G * N * sizeof(float));
     return l;
 }
 
@@ -304,6 +302,7 @@ __global__ void __launch_bounds__(Tile::THREADS, 3)
 selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
     constexpr int K = Tile::K, S = Tile::S, T = Tile::T, GT = Tile::GT, W = Tile::W, THREADS = Tile::THREADS;
     constexpr int Np = Tile::Np, P = Tile::P, CT = Tile::CT, YS = Tile::YS, V = CT / 8, ACC = Tile::ACC;
+    constexpr int IT = (T * V + THREADS - 1) / THREADS;        // 8-channel vectors of a tile a thread
     constexpr int R = 8 / S;                                   // tokens of a round of sums over the channels
     extern __shared__ float4 smem4[];
     float4* sd = smem4;                                        // [T][CT / 2]: dt, dt, x, x; later dx, dx, d dt, d dt
@@ -335,6 +334,16 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
         const int c0 = tile * CT, nc = sh.Dg - c0 < CT ? sh.Dg - c0 : CT;
         const int64_t d0 = g * sh.Dg + c0;
         const bool ok = ch < nc;
+        f32x2 A2[2][S / 2], h[2][S / 2], w[2][S / 2], dA[2][S / 2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            load_states<S>(a.A, d0 + ch + e, a.N, n0, ok, A2[e]);
+            times_log2e<S>(A2[e]);
+            load_states<S>(wh, bc * a.D + d0 + ch + e, a.N, n0, ok, h[e]);
+            load_states<S>(wg, bc * a.D + d0 + ch + e, a.N, n0, ok, w[e]);
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) dA[e][s] = 0;
+        }
         for (int i = tid; i < T * V; i += THREADS) {
             const int t = i / V, c = (i % V) * 8;
             float x[8], dt[8], gy[8];
@@ -348,15 +357,18 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
                 sg[t * (CT / 2) + k] = make_float2(gy[2 * j], gy[2 * j + 1]);
             }
         }
-        f32x2 A2[2][S / 2], h[2][S / 2], w[2][S / 2], dA[2][S / 2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            load_states<S>(a.A, d0 + ch + e, a.N, n0, ok, A2[e]);
-            times_log2e<S>(A2[e]);
-            load_states<S>(wh, bc * a.D + d0 + ch + e, a.N, n0, ok, h[e]);
-            load_states<S>(wg, bc * a.D + d0 + ch + e, a.N, n0, ok, w[e]);
-#pragma unroll
-            for (int s = 0; s < S / 2; ++s) dA[e][s] = 0;
+        // the next tile's inputs come into L2 while this one is computed
+        if (tile + sh.split < sh.tiles) {
+            const int64_t dn = d0 + (int64_t)sh.split * CT;
+            const int nn = sh.Dg - (tile + sh.split) * CT < CT ? sh.Dg - (tile + sh.split) * CT : CT;
+            constexpr int LINE = 128 / (int)sizeof(IoT), LINES = (CT + LINE - 1) / LINE;
+            for (int i = tid; i < 4 * nt * LINES; i += THREADS) {
+                const int which = i % 4, c = (i / 4) % LINES * LINE;
+                const int64_t tok = tok0 + i / 4 / LINES;
+                if (c >= nn || (which == 3 && !a.z)) continue;
+                const IoT* p = (const IoT*)(which == 0 ? a.x : which == 1 ? a.dt_raw : which == 2 ? a.dy : a.z);
+                prefetch_l2(p + tok * (which == 3 ? a.zs : a.D) + dn + c);
+            }
         }
         const float Dv0 = ok && a.Dv ? a.Dv[d0 + ch] : 0.f, Dv1 = ok && a.Dv ? a.Dv[d0 + ch + 1] : 0.f;
         __syncthreads();
@@ -371,9 +383,10 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
                         ((ulonglong2*)hs)[((tg - 1) * (S / 2) + e * (S / 4) + s / 2) * THREADS + tid] =
                             make_ulonglong2(h[e][s], h[e][s + 1]);
             }
+            float y[2 * GT];                                   // token u, channel e
 #pragma unroll
-            for (int r0 = 0; r0 < GT; r0 += R < GT ? R : GT) {
-                float dC[8], y[2 * R];
+            for (int r0 = 0; r0 < GT; r0 += R) {
+                float dC[8];
 #pragma unroll
                 for (int u = 0; u < R; ++u) {
                     const int t = tg * GT + r0 + u;
@@ -395,7 +408,7 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
                             c[s] = e ? f2_fma(gy, h[e][s], c[s]) : f2_mul(gy, h[e][s]);
                         }
                         const float2 yy = f2_get(ys);
-                        y[u * 2 + e] = yy.x + yy.y;
+                        y[(r0 + u) * 2 + e] = yy.x + yy.y;
                     }
 #pragma unroll
                     for (int s = 0; s < S / 2; ++s) {
@@ -405,18 +418,37 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
                     }
                 }
                 put_sums<Tile>(dC, lane, wrow + (tg * GT + r0) * Np);
-                if (a.z) {
+            }
+            if (a.z) {
+                float* out = sy + tg * GT * YS + ch;
+                if constexpr (GT == 4 && K <= 4) {
+                    const int first = sum_over_states<K>(y, lane);
 #pragma unroll
-                    for (int i = 0; i < 2 * R; ++i) {
+                    for (int i = 0; i < 4 / K; ++i) *(float2*)(out + (first / 2 + i) * YS) = make_float2(y[2 * i], y[2 * i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * GT; ++i) {
 #pragma unroll
                         for (int o = P; o < 32; o <<= 1) y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
                     }
                     if (n0 == 0) {
 #pragma unroll
-                        for (int u = 0; u < R; ++u)
-                            *(float2*)(sy + (tg * GT + r0 + u) * YS + ch) = make_float2(y[2 * u], y[2 * u + 1]);
+                        for (int u = 0; u < GT; ++u) *(float2*)(out + u * YS) = make_float2(y[2 * u], y[2 * u + 1]);
                     }
                 }
+            }
+        }
+        // dz; its inputs are loaded on this side of the barrier
+        Raw8<IoT> rz[IT], ry[IT], rx[IT];
+        if (a.z) {
+#pragma unroll
+            for (int q = 0; q < IT; ++q) {
+                const int i = tid + q * THREADS, t = i / V, c = (i % V) * 8;
+                if (t >= nt || c >= nc) continue;
+                const int64_t at = (tok0 + t) * a.D + d0 + c;
+                rz[q].load((const IoT*)a.z + (tok0 + t) * a.zs + d0 + c);
+                ry[q].load((const IoT*)a.dy + at);
+                rx[q].load((const IoT*)a.x + at);
             }
         }
         __syncthreads();
@@ -429,14 +461,15 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
             }
         }
         if (a.z) {
-            for (int i = tid; i < nt * V; i += THREADS) {
-                const int t = i / V, c = (i % V) * 8;
-                if (c >= nc) continue;
+#pragma unroll
+            for (int q = 0; q < IT; ++q) {
+                const int i = tid + q * THREADS, t = i / V, c = (i % V) * 8;
+                if (t >= nt || c >= nc) continue;
                 const int64_t at = (tok0 + t) * a.D + d0 + c;
                 float z[8], dy[8], x[8], dz[8], Dv[8];
-                load8((const IoT*)a.z + (tok0 + t) * a.zs + d0 + c, z);
-                load8((const IoT*)a.dy + at, dy);
-                load8((const IoT*)a.x + at, x);
+                rz[q].get(z);
+                ry[q].get(dy);
+                rx[q].get(x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) Dv[j] = 0.f;
                 if (a.Dv) load8(a.Dv + d0 + c, Dv);
@@ -558,6 +591,12 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             store_states<S>((float*)(a.ws + sh.off_dA), bc * a.D + d0 + ch + e, a.N, n0, ok, dA[e]);
+        Raw8<IoT> rdt[IT];
+#pragma unroll
+        for (int q = 0; q < IT; ++q) {
+            const int i = tid + q * THREADS, t = i / V, c = (i % V) * 8;
+            if (t < nt && c < nc) rdt[q].load((const IoT*)a.dt_raw + (tok0 + t) * a.D + d0 + c);
+        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < ACC; ++i) {
@@ -567,12 +606,13 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
                 for (int q = 0; q < W; ++q) accB[i] += acc[q * T * Np + k];
             }
         }
-        for (int i = tid; i < nt * V; i += THREADS) {
-            const int t = i / V, c = (i % V) * 8;
-            if (c >= nc) continue;
+#pragma unroll
+        for (int q = 0; q < IT; ++q) {
+            const int i = tid + q * THREADS, t = i / V, c = (i % V) * 8;
+            if (t >= nt || c >= nc) continue;
             const int64_t at = (tok0 + t) * a.D + d0 + c;
             float raw[8], bias[8], dx[8], ddt[8];
-            load8((const IoT*)a.dt_raw + at, raw);
+            rdt[q].get(raw);
 #pragma unroll
             for (int j = 0; j < 8; ++j) bias[j] = 0.f;
             if (a.dt_bias) load8(a.dt_bias + d0 + c, bias);
@@ -598,6 +638,7 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
             const float* p = which ? (const float*)(sg + k) + e : (const float*)(sd + (k ^ ((k >> 3) & 7))) + 2 + e;
             const int step = which ? CT : 2 * CT;
             float s = 0.f;
+#pragma unroll 8
             for (int t = 0; t < nt; ++t) s += p[t * step];
             ((float*)(a.ws + sh.off_par))[(bc * 2 + which) * a.D + d0 + c] = s;
         }
@@ -607,9 +648,10 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
     for (int i = 0; i < ACC; ++i) {
         const int k = tid + i * THREADS, t = k / Np, n = k % Np;
         if (k >= T * Np || t >= nt || n >= a.N) continue;
-        const int64_t at = ((int64_t)sp * a.batch * a.L + tok0 + t) * a.G * a.N + g * a.N + n;
-        ((float*)(a.ws + sh.off_dB))[at] = accB[i];
-        ((float*)(a.ws + sh.off_dC))[at] = accC[i];
+        const int64_t all = a.batch * a.L * a.G * a.N;
+        float* out = (float*)(a.ws + sh.off_dBC) + 2 * sp * all + ((tok0 + t) * a.G + g) * a.N + n;
+        out[0] = accB[i];
+        out[all] = accC[i];
     }
 }
 
@@ -646,14 +688,10 @@ static cudaError_t launch_bwd_t(const SelectiveArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t bn = a.batch * sh.nch, DN = a.D * a.N, M = a.batch * a.L * a.G * a.N;
-    const bool gb = sizeof(GT) == 2;
-    const float* par = (const float*)(a.ws + sh.off_par);
-    e = launch_column_sum((const float*)(a.ws + sh.off_dA), bn, DN, DN, a.dA, false, s);
-    if (e == cudaSuccess && a.ddt_bias) e = launch_column_sum(par, bn, 2 * a.D, a.D, a.ddt_bias, false, s);
-    if (e == cudaSuccess && a.dD) e = launch_column_sum(par + a.D, bn, 2 * a.D, a.D, a.dD, false, s);
-    if (e == cudaSuccess) e = launch_column_sum((const float*)(a.ws + sh.off_dB), sh.split, M, M, a.dB, gb, s);
-    if (e == cudaSuccess) e = launch_column_sum((const float*)(a.ws + sh.off_dC), sh.split, M, M, a.dC, gb, s);
-    return e;
+    const ColumnSum sums[] = {{(const float*)(a.ws + sh.off_dBC), sh.split, 2 * M, 2 * M, a.dB, M, a.dC, sizeof(GT) == 2},
+                              {(const float*)(a.ws + sh.off_dA), bn, DN, DN, a.dA, DN, nullptr, false},
+                              {(const float*)(a.ws + sh.off_par), bn, 2 * a.D, 2 * a.D, a.ddt_bias, a.D, a.dD, false}};
+    return launch_column_sums(sums, a.ddt_bias || a.dD ? 3 : 2, s);
 }
 
 template <typename IoT, typename GT>

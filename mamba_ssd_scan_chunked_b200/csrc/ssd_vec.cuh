@@ -19,6 +19,9 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
     Vec16<float>::store(p, v);
     Vec16<float>::store(p + 4, v + 4);
 }
+// asks for the 128-byte line at p to be brought into L2
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // 4 consecutive elements (aligned to their size) to and from fp32.
 __device__ __forceinline__ void load4(const bf16* p, float* v) {
     const uint2 r = *reinterpret_cast<const uint2*>(p);
