@@ -145,9 +145,9 @@ conv1d_fwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
             f32x2 v = bias[i];
 #pragma unroll
             for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], ring[(u + 4 - (W - 1) + k) % 4][i], v);
-            const float2 r = f2_get(v);
-            out[2 * i] = a.silu ? r.x * sigmoid_f32(r.x) : r.x;
-            out[2 * i + 1] = a.silu ? r.y * sigmoid_f32(r.y) : r.y;
+            const float2 r = f2_get(a.silu ? f2_silu(v) : v);
+            out[2 * i] = r.x;
+            out[2 * i + 1] = r.y;
         }
         store4(y + (int64_t)(t + u) * ld, out);
     };
@@ -308,8 +308,7 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
                     f32x2 v = bias[i];
 #pragma unroll
                     for (int k = 0; k < W; ++k) v = f2_fma(w[k][i], ring[(u + 4 - (W - 1) + k) % 4][i], v);
-                    const float2 r = f2_get(v);
-                    dv[i] = f2_mul(dv[i], f2_pack(silu_grad(r.x, sigmoid_f32(r.x)), silu_grad(r.y, sigmoid_f32(r.y))));
+                    dv[i] = f2_mul(dv[i], f2_silu_grad(v, f2_sigmoid(v)));
                 }
                 if (mine) {
                     db[i] = f2_fma(dv[i], f2_pack(1.f, 1.f), db[i]);

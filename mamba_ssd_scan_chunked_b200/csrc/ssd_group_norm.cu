@@ -47,14 +47,15 @@ __device__ __forceinline__ void slot_sum(float (&v)[K], const NormShape& sh, flo
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     if constexpr (!WARP) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = sh.lanes >> 5, first = warp / per * per;
+        const int width = per <= 2 ? 1 : per <= 4 ? 3 : per <= 8 ? 7 : per <= 16 ? 15 : 31;   // a power of two of lanes, less 1
         if (lane == 0)
 #pragma unroll
             for (int k = 0; k < K; ++k) red[turn][warp][k] = v[k];
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = lane < per ? red[turn][first + lane][k] : 0.f;
+        for (int k = 0; k < K; ++k) v[k] = (lane & width) < per ? red[turn][first + (lane & width)][k] : 0.f;
         turn ^= 1;
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = (width + 1) >> 1; o > 0; o >>= 1)
 #pragma unroll
             for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
@@ -114,9 +115,12 @@ group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
     int turn = 0;
     Raw8<XT> nx[NV];
     Raw8<IoT> nz[NV];
+    // a slot's items lie step apart, whole rows
+    const int64_t xstep = at.step * sh.gs, zstep = at.step / a.G * a.zs;
+    const XT* xp = (const XT*)a.x + at.first * sh.gs;
+    const IoT* zp = (const IoT*)a.z + at.first / a.G * a.zs + base;
+    YT* yp = (YT*)a.y + at.first * sh.gs;
     auto load = [&](int64_t item) {
-        const XT* xp = (const XT*)a.x + item * sh.gs;
-        const IoT* zp = (const IoT*)a.z + item / a.G * a.zs + base;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
             const int i = (at.lane + q * sh.lanes) * 8;
@@ -127,6 +131,8 @@ group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 if (a.act >= kAfter) nz[q].load(zp + i);
             }
         }
+        xp += xstep;
+        zp += zstep;
     };
     load(at.first);
     // every thread of a block takes part in its sums, with or without an item
@@ -139,7 +145,11 @@ group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
             if (a.act >= kAfter) {
                 nz[q].get(gate[q]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) gate[q][j] *= sigmoid_f32(gate[q][j]);
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 v = f2_get(f2_silu(f2_pack(gate[q][j], gate[q][j + 1])));
+                    gate[q][j] = v.x;
+                    gate[q][j + 1] = v.y;
+                }
                 if (a.act == kBefore)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) u[q][j] *= gate[q][j];
@@ -167,8 +177,9 @@ group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 const float v = u[q][j];
                 y[j] = a.act == kSilu ? v * sigmoid_f32(v) : a.act == kAfter ? v * gate[q][j] : v;
             }
-            store8((YT*)a.y + item * sh.gs + i, y);
+            store8(yp + i, y);
         }
+        yp += xstep;
     }
 }
 
@@ -187,10 +198,13 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
         for (int j = 0; j < 8; ++j) dw[q][j] = db[q][j] = 0.f;
     Raw8<XT> nx[NV];
     Raw8<IoT> nz[NV], ny[NV];
+    const int64_t xstep = at.step * sh.gs, zstep = at.step / a.G * a.zs;
+    const XT* xp = (const XT*)a.x + at.first * sh.gs;
+    const IoT* yp = (const IoT*)a.dy + at.first * sh.gs;
+    const IoT* zp = (const IoT*)a.z + at.first / a.G * a.zs + base;
+    GT* dxp = (GT*)a.dx + at.first * sh.gs;
+    GT* dzp = (GT*)a.dz + at.first * sh.gs;
     auto load = [&](int64_t item) {
-        const XT* xp = (const XT*)a.x + item * sh.gs;
-        const IoT* yp = (const IoT*)a.dy + item * sh.gs;
-        const IoT* zp = (const IoT*)a.z + item / a.G * a.zs + base;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
             const int i = (at.lane + q * sh.lanes) * 8;
@@ -203,6 +217,9 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 if (a.act >= kAfter) nz[q].load(zp + i);
             }
         }
+        xp += xstep;
+        yp += xstep;
+        zp += zstep;
     };
     load(at.first);
     for (int64_t it0 = (int64_t)blockIdx.x * sh.per_block; it0 < sh.items; it0 += at.step) {
@@ -217,12 +234,26 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 float z[8];
                 nz[q].get(z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float g = sigmoid_f32(z[j]);
-                    s[q][j] = z[j] * g;
-                    t[q][j] = silu_grad(z[j], g) * (a.act == kBefore ? u[q][j] : dn[q][j]);
-                    if (a.act == kBefore) u[q][j] *= s[q][j];
-                    else dn[q][j] *= s[q][j];               // dv
+                for (int j = 0; j < 8; j += 2) {
+                    const f32x2 zz = f2_pack(z[j], z[j + 1]), g = f2_sigmoid(zz);
+                    const float2 sv = f2_get(f2_mul(zz, g)), tv = f2_get(f2_silu_grad(zz, g));
+                    s[q][j] = sv.x;
+                    s[q][j + 1] = sv.y;
+                    t[q][j] = tv.x;
+                    t[q][j + 1] = tv.y;
+                }
+                if (a.act == kBefore) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        t[q][j] *= u[q][j];
+                        u[q][j] *= s[q][j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        t[q][j] *= dn[q][j];
+                        dn[q][j] *= s[q][j];                // dv
+                    }
                 }
             }
         }
@@ -289,7 +320,7 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 if (a.bias) load8(a.bias + base + i, bias);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) g[j] = t[q][j] * fmaf(u[q][j], w[j], bias[j]);
-                store8((GT*)a.dz + item * sh.gs + i, g);
+                store8(dzp + i, g);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -301,9 +332,11 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                     g[j] *= s[q][j];
                 }
             }
-            store8((GT*)a.dx + item * sh.gs + i, g);
-            if (a.act == kBefore) store8((GT*)a.dz + item * sh.gs + i, t[q]);
+            store8(dxp + i, g);
+            if (a.act == kBefore) store8(dzp + i, t[q]);
         }
+        dxp += xstep;
+        dzp += xstep;
     }
     // slot q's sums: row q / G of [slots / G][C]
     float* part = a.ws + at.first * sh.gs;

@@ -78,6 +78,19 @@ __device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
     return r;
 }
 
+// 1 / (1 + e^-v) of both, v / (1 + e^-v) of both, and the latter's derivative from the former
+__device__ __forceinline__ f32x2 f2_sigmoid(f32x2 v) {
+    const float2 t = f2_get(f2_mul(v, f2_pack(-kLog2e, -kLog2e)));
+    const f32x2 one = f2_pack(1.f, 1.f);
+    const float2 q = f2_get(f2_fma(f2_pack(exp2_approx(t.x), exp2_approx(t.y)), one, one));
+    return f2_pack(rcp_approx(q.x), rcp_approx(q.y));
+}
+__device__ __forceinline__ f32x2 f2_silu(f32x2 v) { return f2_mul(v, f2_sigmoid(v)); }
+__device__ __forceinline__ f32x2 f2_silu_grad(f32x2 v, f32x2 g) {
+    const f32x2 one = f2_pack(1.f, 1.f), rest = f2_fma(g, f2_pack(-1.f, -1.f), one);
+    return f2_mul(g, f2_fma(v, rest, one));
+}
+
 // 8 elements as they lie in memory, widened when they are used
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16> {
