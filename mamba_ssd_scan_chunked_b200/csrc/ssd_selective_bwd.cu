@@ -23,8 +23,8 @@
 
 namespace ssd {
 
-// A lane of the third step holds S states of 2 channels, so that half of the
-// sums of dB and dC over the channels are formed in registers.
+// A lane holds S states of 2 channels: B and C are read for both at once, and half
+// of the sums of dB and dC over the channels are formed in registers.
 template <int K_, int S_, int T_, int GT_>
 struct SbTile {
     static constexpr int K = K_;             // lanes of a channel
@@ -44,7 +44,6 @@ struct SbTile {
 
 struct SbShape {
     int Dg, tiles;               // channels of a group, tiles that cover them
-    int tiles1;                  // the same with the tiles of the summaries
     int nch;                     // chunks of a sequence
     int split;                   // blocks that share a chunk's tiles of channels
     size_t off_h, off_g;         // fp32 [b][nch][D][N] chunk states, then adjoints
@@ -57,17 +56,15 @@ struct SbShape {
 
 static int sb_tokens(int64_t N) { return N <= 8 ? 16 : N <= 32 ? 32 : N <= 128 ? 16 : 8; }
 static int sb_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : N <= 64 ? 16 : 8; }
-static int sum_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : N <= 128 ? 16 : 8; }
 
 static SbShape sb_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
     SbShape l{};
-    const int T = sb_tokens(N), CT = sb_channels(N), C1 = sum_channels(N);
+    const int T = sb_tokens(N), CT = sb_channels(N);
     l.Dg = (int)(D / G);
     l.tiles = (l.Dg + CT - 1) / CT;
-    l.tiles1 = (l.Dg + C1 - 1) / C1;
     l.nch = (int)((L + T - 1) / T);
     // 3 blocks an SM; several rounds of them, so that the last one does not leave most SMs idle
-    const int64_t chunks = batch * l.nch * G, want = 148 * 3 * 4;
+    const int64_t chunks = batch * l.nch * G, want = 148 * 3 * 8;
     int64_t split = chunks ? (want + chunks - 1) / chunks : 1;
     if (split > l.tiles) split = l.tiles;
     l.split = (int)split;
@@ -154,17 +151,18 @@ __device__ __forceinline__ void times_log2e(f32x2 (&v)[S / 2]) {
     for (int s = 0; s < S / 2; ++s) v[s] = f2_mul(v[s], f2_pack(kLog2e, kLog2e));
 }
 
-// Step 1 (lanes as in the forward scan: S states of one channel).
-template <typename IoT, class Tile, int T>
-__global__ void __launch_bounds__(Tile::W * 32)
+// Step 1.
+template <typename IoT, class Tile>
+__global__ void __launch_bounds__(Tile::THREADS)
 selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh) {
-    constexpr int S = Tile::S, Np = Tile::Np, CT = Tile::CT, P = Tile::P, THREADS = Tile::W * 32, V = CT / 8;
+    constexpr int S = Tile::S, Np = Tile::Np, CT = Tile::CT, P = Tile::P, T = Tile::T, THREADS = Tile::THREADS, V = CT / 8;
     extern __shared__ float4 smem4[];
-    float4* sd = smem4;                                  // [T][CT]: dt, dt x, g
-    float* sB = (float*)(sd + T * CT);
+    float4* sd = smem4;                                  // [T][CT / 2]: dt, dt, dt x, dt x
+    float2* sg = (float2*)(sd + T * (CT / 2));           // [T][CT / 2]: g, g
+    float* sB = (float*)(sg + T * (CT / 2));
     float* sC = sB + T * Np;
-    const int tile = (int)(blockIdx.x % (unsigned)sh.tiles1);
-    int64_t r = blockIdx.x / (unsigned)sh.tiles1;
+    const int tile = (int)(blockIdx.x % (unsigned)sh.tiles);
+    int64_t r = blockIdx.x / (unsigned)sh.tiles;
     const int64_t g = r % a.G;
     r /= a.G;
     const int64_t ck = r % sh.nch, b = r / sh.nch, t0 = ck * T, bc = b * sh.nch + ck;
@@ -172,50 +170,66 @@ selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh) {
     const int c0 = tile * CT, nc = sh.Dg - c0 < CT ? sh.Dg - c0 : CT;
     const int64_t d0 = g * sh.Dg + c0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ch = warp * P + lane % P, n0 = (lane / P) * S;
+    const int pair = warp * P + lane % P, n0 = (lane / P) * S, ch = pair * 2;
     const bool ok = ch < nc;
+    f32x2 A2[2][S / 2], h[2][S / 2], Pr[2][S / 2], Gs[2][S / 2];
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        load_states<S>(a.A, d0 + ch + e, a.N, n0, ok, A2[e]);
+        times_log2e<S>(A2[e]);
+#pragma unroll
+        for (int s = 0; s < S / 2; ++s) {
+            h[e][s] = Gs[e][s] = 0;
+            Pr[e][s] = f2_pack(1.f, 1.f);
+        }
+    }
     for (int i = threadIdx.x; i < T * V; i += THREADS) {
         const int t = i / V, c = (i % V) * 8;
         float x[8], dt[8], gy[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = dt[j] = gy[j] = 0.f;
         if (t < nt && c < nc) load_token<IoT>(a, b * a.L + t0 + t, d0 + c, x, dt, gy);
-        // channel k lies at k ^ (k >> 3): the vectors of 8 threads then meet all banks
+        // pair k lies at k ^ (k >> 3): the vectors of 8 threads then meet all banks
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sd[t * CT + ((c + j) ^ (((c + j) >> 3) & 7))] = make_float4(dt[j], dt[j] * x[j], gy[j], 0.f);
+        for (int j = 0; j < 4; ++j) {
+            const int k = c / 2 + j;
+            sd[t * (CT / 2) + (k ^ ((k >> 3) & 7))] =
+                make_float4(dt[2 * j], dt[2 * j + 1], dt[2 * j] * x[2 * j], dt[2 * j + 1] * x[2 * j + 1]);
+            sg[t * (CT / 2) + k] = make_float2(gy[2 * j], gy[2 * j + 1]);
+        }
     }
     stage_bc<IoT, T, Np, THREADS>(a, b, g, t0, nt, sB, sC);
-    f32x2 A2[S / 2], h[S / 2], Pr[S / 2], Gs[S / 2];
-    load_states<S>(a.A, d0 + ch, a.N, n0, ok, A2);
-    times_log2e<S>(A2);
-    float sum = 0.f;
-#pragma unroll
-    for (int s = 0; s < S / 2; ++s) {
-        h[s] = Gs[s] = 0;
-        Pr[s] = f2_pack(1.f, 1.f);
-    }
     __syncthreads();
-    const float4* pd = sd + (ch ^ ((ch >> 3) & 7));
+    const float4* pd = sd + (pair ^ ((pair >> 3) & 7));
+    const float2* pg = sg + pair;
 #pragma unroll 4
     for (int t = 0; t < T; ++t) {                        // tokens past the end have dt = 0 and g = 0
-        const float4 d = pd[t * CT];
+        const float4 d = pd[t * (CT / 2)];
+        const float2 g2 = pg[t * (CT / 2)];
         f32x2 B[S / 2], C[S / 2];
         f2_load<S>(sB + t * Np + n0, B);
         f2_load<S>(sC + t * Np + n0, C);
-        const f32x2 dt = f2_pack(d.x, d.x), dx = f2_pack(d.y, d.y), gy = f2_pack(d.z, d.z);
-        sum += d.x;
 #pragma unroll
-        for (int s = 0; s < S / 2; ++s) {
-            const f32x2 av = f2_exp2(f2_mul(dt, A2[s]));
-            h[s] = f2_fma(av, h[s], f2_mul(dx, B[s]));
-            Pr[s] = f2_mul(Pr[s], av);
-            Gs[s] = f2_fma(Pr[s], f2_mul(C[s], gy), Gs[s]);
+        for (int e = 0; e < 2; ++e) {
+            const float dt1 = e ? d.y : d.x, dx1 = e ? d.w : d.z, g1 = e ? g2.y : g2.x;
+            const f32x2 dt = f2_pack(dt1, dt1), dx = f2_pack(dx1, dx1), gy = f2_pack(g1, g1);
+            sum[e] += dt1;
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) {
+                const f32x2 av = f2_exp2(f2_mul(dt, A2[e][s]));
+                h[e][s] = f2_fma(av, h[e][s], f2_mul(dx, B[s]));
+                Pr[e][s] = f2_mul(Pr[e][s], av);
+                Gs[e][s] = f2_fma(Pr[e][s], f2_mul(C[s], gy), Gs[e][s]);
+            }
         }
     }
-    store_states<S>((float*)(a.ws + sh.off_h), bc * a.D + d0 + ch, a.N, n0, ok, h);
-    store_states<S>((float*)(a.ws + sh.off_g), bc * a.D + d0 + ch, a.N, n0, ok, Gs);
-    if (ok && n0 == 0) ((float*)(a.ws + sh.off_dt))[bc * a.D + d0 + ch] = sum;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        store_states<S>((float*)(a.ws + sh.off_h), bc * a.D + d0 + ch + e, a.N, n0, ok, h[e]);
+        store_states<S>((float*)(a.ws + sh.off_g), bc * a.D + d0 + ch + e, a.N, n0, ok, Gs[e]);
+        if (ok && n0 == 0) ((float*)(a.ws + sh.off_dt))[bc * a.D + d0 + ch + e] = sum[e];
+    }
 }
 
 // Step 2, a thread a state: the first half of the blocks turns the chunks' end
@@ -669,12 +683,12 @@ __global__ void selective_bwd_empty_kernel(const SelectiveArgs a) {
     }
 }
 
-template <typename IoT, typename GT, class Sum, class Main>
+template <typename IoT, typename GT, class Tile>
 static cudaError_t launch_bwd_t(const SelectiveArgs& a, cudaStream_t s) {
     const SbShape sh = sb_shape(a.batch, a.L, a.D, a.N, a.G);
-    constexpr int smem1 = (int)sizeof(float) * Main::T * (4 * Sum::CT + 2 * Sum::Np), smem3 = Main::SMEM;
-    const auto k1 = selective_bwd_summary_kernel<IoT, Sum, Main::T>;
-    const auto k3 = selective_bwd_main_kernel<IoT, GT, Main>;
+    constexpr int smem1 = (int)sizeof(float) * Tile::T * (3 * Tile::CT + 2 * Tile::Np), smem3 = Tile::SMEM;
+    const auto k1 = selective_bwd_summary_kernel<IoT, Tile>;
+    const auto k3 = selective_bwd_main_kernel<IoT, GT, Tile>;
     cudaError_t e = cudaSuccess;
     if (smem1 > 48 * 1024) e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
     if (e == cudaSuccess && smem3 > 48 * 1024)
@@ -682,9 +696,9 @@ static cudaError_t launch_bwd_t(const SelectiveArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t chunks = a.batch * sh.nch * a.G;
     const int half = (int)((a.batch * a.D * a.N + 127) / 128);
-    k1<<<(unsigned)(chunks * sh.tiles1), Sum::W * 32, smem1, s>>>(a, sh);
+    k1<<<(unsigned)(chunks * sh.tiles), Tile::THREADS, smem1, s>>>(a, sh);
     selective_bwd_chunks_kernel<<<(unsigned)(2 * half), 128, 0, s>>>(a, sh, half);
-    k3<<<(unsigned)(chunks * sh.split), Main::THREADS, smem3, s>>>(a, sh);
+    k3<<<(unsigned)(chunks * sh.split), Tile::THREADS, smem3, s>>>(a, sh);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t bn = a.batch * sh.nch, DN = a.D * a.N, M = a.batch * a.L * a.G * a.N;
@@ -696,12 +710,12 @@ static cudaError_t launch_bwd_t(const SelectiveArgs& a, cudaStream_t s) {
 
 template <typename IoT, typename GT>
 static cudaError_t launch_bwd_s(const SelectiveArgs& a, cudaStream_t s) {
-    if (a.N <= 8) return launch_bwd_t<IoT, GT, SelTile<2, 4, 8>, SbTile<2, 4, 16, 4>>(a, s);
-    if (a.N <= 16) return launch_bwd_t<IoT, GT, SelTile<4, 4, 8>, SbTile<4, 4, 32, 4>>(a, s);
-    if (a.N <= 32) return launch_bwd_t<IoT, GT, SelTile<8, 4, 8>, SbTile<8, 4, 32, 4>>(a, s);
-    if (a.N <= 64) return launch_bwd_t<IoT, GT, SelTile<16, 4, 8>, SbTile<16, 4, 16, 4>>(a, s);
-    if (a.N <= 128) return launch_bwd_t<IoT, GT, SelTile<32, 4, 16>, SbTile<32, 4, 16, 4>>(a, s);
-    return launch_bwd_t<IoT, GT, SelTile<32, 8, 8>, SbTile<32, 8, 8, 2>>(a, s);
+    if (a.N <= 8) return launch_bwd_t<IoT, GT, SbTile<2, 4, 16, 4>>(a, s);
+    if (a.N <= 16) return launch_bwd_t<IoT, GT, SbTile<4, 4, 32, 4>>(a, s);
+    if (a.N <= 32) return launch_bwd_t<IoT, GT, SbTile<8, 4, 32, 4>>(a, s);
+    if (a.N <= 64) return launch_bwd_t<IoT, GT, SbTile<16, 4, 16, 4>>(a, s);
+    if (a.N <= 128) return launch_bwd_t<IoT, GT, SbTile<32, 4, 16, 4>>(a, s);
+    return launch_bwd_t<IoT, GT, SbTile<32, 8, 8, 2>>(a, s);
 }
 
 cudaError_t launch_selective_bwd(const SelectiveArgs& a, cudaStream_t s) {

@@ -822,22 +822,24 @@ def _workspace(workspace, need, x):
 
 
 def _silu_flag(activation) -> int:
-    if activation not in (None, "silu"):
+    if activation is None:
+        return 0
+    if activation != "silu":
         raise ValueError(f"activation: {activation!r}, expected None or 'silu'")
-    return 0 if activation is None else 1
+    return 1
 
 
 def _split_widths(split, channels):
-    widths = (channels,) if split is None else tuple(split)
+    if split is None:
+        return (channels,)
+    widths = tuple(split)
     if not 1 <= len(widths) <= 3 or min(widths) < 1 or sum(widths) != channels:
         raise ValueError(f"split: {split}, expected one to three widths that add up to {channels} channels")
     return widths
 
 
 def _conv_outputs(y, widths, lead, dtype, one):
-    """The given outputs, checked, or None for each."""
-    if y is None:
-        return [None] * len(widths)
+    """The given outputs, checked."""
     y = [y] if one and hasattr(y, "shape") else list(y)
     if len(y) != len(widths):
         raise ValueError(f"y: {len(y)} tensors, expected {len(widths)}")
@@ -848,7 +850,8 @@ def _conv_outputs(y, widths, lead, dtype, one):
 
 def _three(tensors):
     """The addresses of up to three tensors, 0 for those that are not there."""
-    return [t.data_ptr() for t in tensors] + [0] * (3 - len(tensors))
+    n = len(tensors)
+    return (tensors[0].data_ptr(), tensors[1].data_ptr() if n > 1 else 0, tensors[2].data_ptr() if n > 2 else 0)
 
 
 def _conv_desc(b, L, D, W, xs, dxs, widths, io, y, state, activation) -> Conv1dDesc:
@@ -883,12 +886,12 @@ def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation=
     _check(init_state, kept, "init_state", state_dtype)
     _check(final_state, kept, "final_state", state_dtype)
     _check(pad_left, (b,), "pad_left", torch.int32)
-    out = _conv_outputs(y, widths, (b, L), y_dtype, split is None)
+    out = _conv_outputs(y, widths, (b, L), y_dtype, split is None) if y is not None else ()
     desc = _conv_desc(b, L, D, W, xs, D, widths, x.dtype, y_dtype, state_dtype, activation)
     device = _one_device((weight, bias, init_state, pad_left, final_state, *out), (x,))
 
     def call(handle):
-        ys = [x.new_empty((b, L, n), dtype=y_dtype) if t is None else t for t, n in zip(out, widths)]
+        ys = out if y is not None else [x.new_empty((b, L, n), dtype=y_dtype) for n in widths]
         final = final_state
         if final is None and want_final_state:
             final = x.new_empty(kept, dtype=state_dtype)
@@ -914,12 +917,12 @@ def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu",
     _check(weight, (D, W), "weight", torch.float32)
     _check(bias, (D,), "bias", torch.float32)
     _check(state, (b, W - 1, D), "state")
-    out = _conv_outputs(y, widths, (b,), y_dtype, split is None)
+    out = _conv_outputs(y, widths, (b,), y_dtype, split is None) if y is not None else ()
     desc = _conv_desc(b, 1, D, W, xs, D, widths, x.dtype, y_dtype, state.dtype, activation)
     device = _one_device((state, weight, bias, *out), (x,))
 
     def call(handle):
-        ys = [x.new_empty((b, n), dtype=y_dtype) if t is None else t for t, n in zip(out, widths)]
+        ys = out if y is not None else [x.new_empty((b, n), dtype=y_dtype) for n in widths]
         st = ssd_conv1d_update(desc, state.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), *_three(ys), handle)
         if st:
             raise SsdError(st, "ssd_conv1d_update")
@@ -1109,17 +1112,18 @@ def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=No
 
 
 def _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype) -> GroupNormDesc:
-    import torch
-    lead, C = tuple(x.shape[:-1]), x.shape[-1]
-    _check(weight, (C,), "weight", torch.float32)
-    _check(bias, (C,), "bias", torch.float32)
+    *lead, C = x.shape
     act, zs, rows = _silu_flag(activation), C, 1
     for n in lead:
         rows *= n
+    if weight is not None or bias is not None:
+        import torch
+        _check(weight, (C,), "weight", torch.float32)
+        _check(bias, (C,), "bias", torch.float32)
     if z is not None:
         if act:
             raise ValueError("activation: the gate z has its own SiLU")
-        zs = _row_stride(z, "z", lead, C, io_dtype)
+        zs = _row_stride(z, "z", tuple(lead), C, io_dtype)
         act = SSD_NORM_GATE_BEFORE if gate_first else SSD_NORM_GATE_AFTER
     return GroupNormDesc(rows, C, ngroups, zs, eps, _code(x.dtype), _code(io_dtype), _code(y_dtype),
                          1 if center else 0, act)
@@ -1134,7 +1138,6 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, ce
     the result is multiplied by silu(z); without one ``activation`` may be "silu".  Returns y [..., C]
     (``y_dtype``, default z's dtype, else x's).
     """
-    import torch
     io_dtype = z.dtype if z is not None else x.dtype
     if y_dtype is None:
         y_dtype = y.dtype if y is not None else io_dtype

@@ -135,7 +135,7 @@ def test_selective_state_update_bf16_state_rounds_once(b, D, N):
     (2, 1, 16, 16, 1, B, B, B, True, True, True, True, 0),
     (2, 0, 16, 16, 1, F, F, F, True, True, True, True, 0),
     (0, 4, 16, 16, 1, F, F, F, False, False, True, False, 0),
-    (4, 7190, 136, 8, 1, B, B, F, True, True, True, True, 8),            # so many chunks that a block takes two tiles
+    (8, 7190, 136, 8, 1, B, B, F, True, True, True, True, 8),            # so many chunks that a block takes two tiles
     (4, 130, 272, 16, 2, F, F, F, True, True, True, True, 0),            # several tiles of channels in two groups
 ])
 def test_selective_scan_bwd(b, L, D, N, G, io, g, state, init, gate, skip, dfinal, extra):
