@@ -99,30 +99,42 @@ __device__ __forceinline__ void stage_bc(const SelectiveArgs& a, int64_t b, int6
     }
 }
 
-// x, dt and g of 8 channels of a token
-template <typename IoT>
-__device__ __forceinline__ void load_token(const SelectiveArgs& a, int64_t tok, int64_t d, float (&x)[8], float (&dt)[8],
-                                           float (&g)[8]) {
-    float raw[8], bias[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bias[j] = 0.f;
-    load8((const IoT*)a.x + tok * a.D + d, x);
-    load8((const IoT*)a.dt_raw + tok * a.D + d, raw);
-    load8((const IoT*)a.dy + tok * a.D + d, g);
-    if (a.dt_bias) load8(a.dt_bias + d, bias);
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const float2 v = f2_get(softplus2(raw[j] + bias[j], raw[j + 1] + bias[j + 1]));
-        dt[j] = v.x;
-        dt[j + 1] = v.y;
+// 8 channels of a token as they lie in memory, and x, dt and g of them
+template <typename IoT> struct TokenRaw {
+    Raw8<IoT> x, dt, dy, z;
+    __device__ __forceinline__ void load(const SelectiveArgs& a, int64_t tok, int64_t d) {
+        x.load((const IoT*)a.x + tok * a.D + d);
+        dt.load((const IoT*)a.dt_raw + tok * a.D + d);
+        dy.load((const IoT*)a.dy + tok * a.D + d);
+        if (a.z) z.load((const IoT*)a.z + tok * a.zs + d);
     }
-    if (a.z) {
-        float z[8];
-        load8((const IoT*)a.z + tok * a.zs + d, z);
+    __device__ __forceinline__ void get(const SelectiveArgs& a, int64_t d, float (&xv)[8], float (&dtv)[8],
+                                        float (&g)[8]) const {
+        float raw[8], bias[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= z[j] * sigmoid_f32(z[j]);
+        for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+        if (a.dt_bias) load8(a.dt_bias + d, bias);
+        x.get(xv);
+        dt.get(raw);
+        dy.get(g);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float2 v = f2_get(softplus2(raw[j] + bias[j], raw[j + 1] + bias[j + 1]));
+            dtv[j] = v.x;
+            dtv[j + 1] = v.y;
+        }
+        if (a.z) {
+            float zv[8];
+            z.get(zv);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 v = f2_get(f2_mul(f2_pack(g[j], g[j + 1]), f2_silu(f2_pack(zv[j], zv[j + 1]))));
+                g[j] = v.x;
+                g[j + 1] = v.y;
+            }
+        }
     }
-}
+};
 
 // The S floats of a lane's states n0 .. of row `i` of a matrix [..][N] (zero past N)
 template <int S>
@@ -189,7 +201,11 @@ selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh) {
         float x[8], dt[8], gy[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = dt[j] = gy[j] = 0.f;
-        if (t < nt && c < nc) load_token<IoT>(a, b * a.L + t0 + t, d0 + c, x, dt, gy);
+        if (t < nt && c < nc) {
+            TokenRaw<IoT> raw;
+            raw.load(a, b * a.L + t0 + t, d0 + c);
+            raw.get(a, d0 + c, x, dt, gy);
+        }
         // pair k lies at k ^ (k >> 3): the vectors of 8 threads then meet all banks
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -363,7 +379,11 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
             float x[8], dt[8], gy[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = dt[j] = gy[j] = 0.f;
-            if (t < nt && c < nc) load_token<IoT>(a, tok0 + t, d0 + c, x, dt, gy);
+            if (t < nt && c < nc) {
+                TokenRaw<IoT> raw;
+                raw.load(a, tok0 + t, d0 + c);
+                raw.get(a, d0 + c, x, dt, gy);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int k = c / 2 + j;
