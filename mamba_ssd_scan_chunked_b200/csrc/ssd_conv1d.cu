@@ -248,22 +248,22 @@ conv1d_update_kernel(const Conv1dArgs a, int cblocks) {
     }
 }
 
-// Backward.  A block is 32 lanes (4 channels each) x 8 warps; warp q walks over
-// the kBwdTokens tokens of its run and the W - 1 after it (whose dv its last dx
-// need), loads a round ahead.  dx of a token is complete W - 1 tokens later.  The
+// Backward.  A block is 32 lanes (4 channels each) x 4 warps; warp q walks over
+// the tokens of its run and the W - 1 after it (whose dv its last dx need), loads a
+// round ahead.  dx of a token is complete W - 1 tokens later.  The
 // block's sums of dw and db go to one row of the partial sums.
-constexpr int kBwdWarps = 8, kBwdTokens = 64, kBwdRound = 4;
+constexpr int kBwdWarps = 4, kBwdRound = 4;
 
 template <typename IoT, typename GT, int W>
-__global__ void __launch_bounds__(kBwdWarps * 32, 2)
-conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
+__global__ void __launch_bounds__(kBwdWarps * 32, 4)
+conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg, int run) {
     constexpr int H = VEC / 2, U = kBwdRound;
     __shared__ float sums[kBwdWarps][(W + 1) * VEC][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = ((int64_t)(blockIdx.x % (unsigned)cblocks) * 32 + lane) * VEC;
     const int64_t bs = blockIdx.x / (unsigned)cblocks;
     const int64_t b = bs / nseg, seg = bs % nseg;
-    const int64_t t0 = (seg * kBwdWarps + warp) * kBwdTokens;
+    const int64_t t0 = (seg * kBwdWarps + warp) * run;
     f32x2 dw[W][H], db[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) {
@@ -278,7 +278,7 @@ conv1d_bwd_kernel(const Conv1dArgs a, int cblocks, int nseg) {
         const IoT* x = (const IoT*)a.x + (b * a.L + t0) * a.xs + c;
         GT* dx = (GT*)a.dx + (b * a.L + t0) * a.dxs + c;
         const int left = a.L - t0 < (1 << 20) ? (int)(a.L - t0) : 1 << 20;   // tokens from t0 on
-        const int len = left < kBwdTokens ? left : kBwdTokens;
+        const int len = left < run ? left : run;
         Raw4<IoT> nx[U], ny[U];
         auto load = [&](int t) {
 #pragma unroll
@@ -414,12 +414,19 @@ static int fwd_run(int64_t batch, int64_t L, int64_t vecs) { return batch * ((L 
 
 static int64_t fwd_segments(int64_t L, int run) { return L > 0 ? (L + run - 1) / run : 1; }
 
-static int64_t bwd_segments(int64_t L) {
-    const int64_t run = kBwdWarps * kBwdTokens;
-    return L > 0 ? (L + run - 1) / run : 1;
+// tokens a warp of the backward walks over: the longest run that leaves 384 threads
+// an SM (4 x 2048 tokens x 4352 channels: 128 tokens 62 us, 64 tokens 68 us)
+static int bwd_run(int64_t batch, int64_t L, int64_t D) {
+    for (int run = 128; run > 16; run /= 2)
+        if (batch * ((L + run - 1) / run) * (D / VEC) >= 148 * 384) return run;
+    return 16;
 }
 
-int64_t conv1d_bwd_segments(int64_t batch, int64_t L) { return batch * bwd_segments(L); }
+static int64_t bwd_segments(int64_t L, int run) {
+    return L > 0 ? (L + kBwdWarps * run - 1) / (kBwdWarps * run) : 1;
+}
+
+int64_t conv1d_bwd_segments(int64_t batch, int64_t L, int64_t D) { return batch * bwd_segments(L, bwd_run(batch, L, D)); }
 
 int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D) {
     return batch * fwd_segments(L, 8) * ((D / 4 + 31) / 32);
@@ -469,9 +476,10 @@ cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s) {
         conv1d_zero_kernel<<<(unsigned)((nw + a.D + 255) / 256), 256, 0, s>>>(a.dw, a.db, nw, a.D);
         return cudaGetLastError();
     }
-    const int cblocks = (int)((a.D / VEC + 31) / 32), nseg = (int)bwd_segments(a.L);
+    const int cblocks = (int)((a.D / VEC + 31) / 32), run = bwd_run(a.batch, a.L, a.D);
+    const int nseg = (int)bwd_segments(a.L, run);
     const unsigned grid = (unsigned)(a.batch * nseg * cblocks);
-#define FN(IO, G_, W_) conv1d_bwd_kernel<IO, G_, W_><<<grid, kBwdWarps * 32, 0, s>>>(a, cblocks, nseg)
+#define FN(IO, G_, W_) conv1d_bwd_kernel<IO, G_, W_><<<grid, kBwdWarps * 32, 0, s>>>(a, cblocks, nseg, run)
     CONV1D_DISPATCH(FN);
 #undef FN
     const cudaError_t e = cudaGetLastError();

@@ -227,7 +227,7 @@ cudaError_t launch_conv1d_fwd(const Conv1dArgs& a, cudaStream_t s);
 cudaError_t launch_conv1d_update(const Conv1dArgs& a, cudaStream_t s);
 cudaError_t launch_conv1d_bwd(const Conv1dArgs& a, cudaStream_t s);
 // token segments of the backward (rows of its partial sums); 0 for an empty batch
-int64_t conv1d_bwd_segments(int64_t batch, int64_t L);
+int64_t conv1d_bwd_segments(int64_t batch, int64_t L, int64_t D);
 // blocks the forward and backward launch at most (their grids are one-dimensional)
 int64_t conv1d_blocks(int64_t batch, int64_t L, int64_t D);
 

@@ -95,7 +95,7 @@ static ssd_status_t check_selective_desc(const ssd_selective_desc_t* d, bool gat
     if (d->batch > kMaxBatch || d->seqlen > kMaxLen || d->batch * (d->seqlen / 8 + 1) >= kMaxBlocks)
         return SSD_ERR_UNSUPPORTED;
     if (d->batch * (d->seqlen / 8 + 1) * d->ngroups >= kMaxBlocks ||
-        selective_blocks(d->batch, d->seqlen, d->channels, d->dstate, d->ngroups) >= kMaxBlocks)
+        selective_blocks(d->batch, d->seqlen, d->channels, d->dstate, d->ngroups) >= kMaxBlocks / 2)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -193,7 +193,7 @@ ssd_status_t ssd_conv1d_bwd_workspace_size(const ssd_conv1d_desc_t* d, size_t* b
     if (!bytes) return SSD_ERR_INVALID_ARG;
     const ssd_status_t st = check_conv1d_desc(d, true);
     if (st != SSD_OK) return st;
-    *bytes = sizeof(float) * (size_t)conv1d_bwd_segments(d->batch, d->seqlen) * d->channels * (d->width + 1);
+    *bytes = sizeof(float) * (size_t)conv1d_bwd_segments(d->batch, d->seqlen, d->channels) * d->channels * (d->width + 1);
     return SSD_OK;
 }
 
