@@ -36,47 +36,58 @@ struct NormShape {
     int64_t blocks, items;
 };
 
-// Sums K values over the slot's threads; every thread gets them.  Across warps
-// the warps' sums meet in shared memory; `turn` alternates between its two
-// halves, so that one barrier an exchange is enough.
-template <int K, bool WARP>
-__device__ __forceinline__ void slot_sum(float (&v)[K], const NormShape& sh, float (*red)[32][2], int& turn) {
-    const int span = WARP ? sh.lanes : 32;
-    for (int o = span >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if constexpr (!WARP) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = sh.lanes >> 5, first = warp / per * per;
-        const int width = per <= 2 ? 1 : per <= 4 ? 3 : per <= 8 ? 7 : per <= 16 ? 15 : 31;   // a power of two of lanes, less 1
-        if (lane == 0)
-#pragma unroll
-            for (int k = 0; k < K; ++k) red[turn][warp][k] = v[k];
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = (lane & width) < per ? red[turn][first + (lane & width)][k] : 0.f;
-        turn ^= 1;
-        for (int o = (width + 1) >> 1; o > 0; o >>= 1)
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    }
-}
-
-// where a thread stands
+// Where a thread stands, and its way through the sums over its slot: within a
+// warp, then, across the slot's warps, through shared memory, whose two halves take
+// turns, so that one barrier an exchange is enough.
 template <bool WARP> struct Place {
     int slot, lane;
     int64_t first, step;     // the slot's first item, from one of its items to the next
-    __device__ __forceinline__ explicit Place(const NormShape& sh) {
+    int width;               // of the last exchange: a power of two of lanes
+    float (*own)[2];         // this warp's place in red
+    float (*from)[2];        // the place that this lane reads (nullptr: none)
+    __device__ __forceinline__ Place(const NormShape& sh, float (*red)[32][2]) {
         slot = (int)threadIdx.x / sh.lanes;
         lane = (int)threadIdx.x % sh.lanes;
         first = (int64_t)blockIdx.x * sh.per_block + slot;
         step = sh.blocks * sh.per_block;
+        width = sh.lanes;
+        if constexpr (!WARP) {
+            const int warp = threadIdx.x >> 5, per = sh.lanes >> 5, w0 = slot * per;
+            width = per <= 2 ? 2 : per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 ? 16 : 32;
+            const int k = threadIdx.x & (width - 1);
+            own = red[0] + warp;
+            from = k < per ? red[0] + w0 + k : nullptr;
+        }
+    }
+    // sums K values; every thread of the slot gets them
+    template <int K> __device__ __forceinline__ void sum(float (&v)[K], int& turn) const {
+        if constexpr (WARP) {
+            for (int o = width >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int k = 0; k < K; ++k) own[turn][k] = v[k];
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = from ? from[turn][k] : 0.f;
+            turn ^= 32;
+            for (int o = width >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        }
     }
 };
 
 // r and nrm (in the place of u) from u; masked channels of u are 0
 template <int NV, bool WARP>
 __device__ __forceinline__ float normalise(const GroupNormArgs& a, const NormShape& sh, const Place<WARP>& at,
-                                           float (&u)[NV][8], float (*red)[32][2], int& turn) {
+                                           float (&u)[NV][8], int& turn) {
     const float inv = 1.f / (float)sh.gs;
     if (a.center) {
         float s[1] = {0.f};
@@ -84,7 +95,7 @@ __device__ __forceinline__ float normalise(const GroupNormArgs& a, const NormSha
         for (int q = 0; q < NV; ++q)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] += u[q][j];
-        slot_sum<1, WARP>(s, sh, red, turn);
+        at.sum(s, turn);
         const float m = s[0] * inv;
 #pragma unroll
         for (int q = 0; q < NV; ++q)
@@ -97,8 +108,8 @@ __device__ __forceinline__ float normalise(const GroupNormArgs& a, const NormSha
     for (int q = 0; q < NV; ++q)
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss[0] = fmaf(u[q][j], u[q][j], ss[0]);
-    slot_sum<1, WARP>(ss, sh, red, turn);
-    const float r = 1.f / sqrtf(ss[0] * inv + a.eps);
+    at.sum(ss, turn);
+    const float r = rsqrtf(ss[0] * inv + a.eps);
 #pragma unroll
     for (int q = 0; q < NV; ++q)
 #pragma unroll
@@ -110,7 +121,7 @@ template <typename XT, typename IoT, typename YT, int NV, bool WARP, int THREADS
 __global__ void __launch_bounds__(THREADS, norm_blocks_per_sm(false, THREADS))
 group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
     __shared__ float red[2][32][2];
-    const Place<WARP> at(sh);
+    const Place<WARP> at(sh, red);
     const int64_t base = (at.first % a.G) * sh.gs;
     int turn = 0;
     Raw8<XT> nx[NV];
@@ -156,28 +167,35 @@ group_norm_fwd_kernel(const GroupNormArgs a, const NormShape sh) {
             }
         }
         load(item + at.step);
-        normalise<NV, WARP>(a, sh, at, u, red, turn);
+        normalise<NV, WARP>(a, sh, at, u, turn);
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
             const int i = (at.lane + q * sh.lanes) * 8;
             if (item >= sh.items || i >= sh.gs) continue;
-            float w[8], y[8];
             if (a.w) {
+                float w[8];
                 load8(a.w + base + i, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[q][j] *= w[j];
             }
             if (a.bias) {
+                float w[8];
                 load8(a.bias + base + i, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[q][j] += w[j];
             }
+            if (a.act == kAfter) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = u[q][j];
-                y[j] = a.act == kSilu ? v * sigmoid_f32(v) : a.act == kAfter ? v * gate[q][j] : v;
+                for (int j = 0; j < 8; ++j) u[q][j] *= gate[q][j];
+            } else if (a.act == kSilu) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 v = f2_get(f2_silu(f2_pack(u[q][j], u[q][j + 1])));
+                    u[q][j] = v.x;
+                    u[q][j + 1] = v.y;
+                }
             }
-            store8(yp + i, y);
+            store8(yp + i, u[q]);
         }
         yp += xstep;
     }
@@ -187,7 +205,7 @@ template <typename XT, typename IoT, typename GT, int NV, bool WARP, int THREADS
 __global__ void __launch_bounds__(THREADS, norm_blocks_per_sm(true, THREADS))
 group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
     __shared__ float red[2][32][2];
-    const Place<WARP> at(sh);
+    const Place<WARP> at(sh, red);
     const int64_t base = (at.first % a.G) * sh.gs;
     const float inv = 1.f / (float)sh.gs;
     int turn = 0;
@@ -273,15 +291,15 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                     sums[1] = fmaf(dn[q][j] * w[j], u[q][j], sums[1]);
                 }
             }
-            slot_sum<2, WARP>(sums, sh, red, turn);
-            r = 1.f / sqrtf(sums[0] * inv + a.eps);
+            at.sum(sums, turn);
+            r = rsqrtf(sums[0] * inv + a.eps);
             s1 = r * sums[1] * inv;
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[q][j] *= r;
         } else {
-            r = normalise<NV, WARP>(a, sh, at, u, red, turn);
+            r = normalise<NV, WARP>(a, sh, at, u, turn);
             float sums[2] = {0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < NV; ++q) {
@@ -291,17 +309,20 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 for (int j = 0; j < 8; ++j) { w[j] = 1.f; bias[j] = 0.f; }
                 if (a.w && i < sh.gs) load8(a.w + base + i, w);
                 if (a.bias && a.act == kSilu && i < sh.gs) load8(a.bias + base + i, bias);
+                if (a.act == kSilu) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (a.act == kSilu) {
+                    for (int j = 0; j < 8; ++j) {
                         const float v = fmaf(u[q][j], w[j], bias[j]);
                         dn[q][j] *= silu_grad(v, sigmoid_f32(v));
                     }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
                     sums[0] = fmaf(dn[q][j], w[j], sums[0]);
                     sums[1] = fmaf(dn[q][j] * w[j], u[q][j], sums[1]);
                 }
             }
-            slot_sum<2, WARP>(sums, sh, red, turn);
+            at.sum(sums, turn);
             s0 = a.center ? sums[0] * inv : 0.f;
             s1 = sums[1] * inv;
         }
@@ -323,11 +344,16 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
                 store8(dzp + i, g);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[q][j] = fmaf(dn[q][j], u[q][j], dw[q][j]);
-                db[q][j] += dn[q][j];
-                g[j] = r * (fmaf(dn[q][j], w[j], -s0) - u[q][j] * s1);          // du
-                if (a.act == kBefore) {
+            for (int j = 0; j < 8; ++j) dw[q][j] = fmaf(dn[q][j], u[q][j], dw[q][j]);
+            if (a.db)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) db[q][j] += dn[q][j];
+            const float rs0 = r * s0, rs1 = r * s1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = fmaf(-rs1, u[q][j], fmaf(dn[q][j] * r, w[j], -rs0));          // du
+            if (a.act == kBefore) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
                     t[q][j] *= g[j];
                     g[j] *= s[q][j];
                 }
