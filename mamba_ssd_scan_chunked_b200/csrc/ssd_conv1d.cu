@@ -6,7 +6,14 @@
 //
 // Every kernel is a stream bound by HBM: a thread owns a few neighbouring
 // channels, walks over a run of tokens with the last W - 1 inputs in registers,
-// and so reads each input once (and W - 1 more per run).
+// and so reads each input once (and W - 1 more per run).  The inputs stand in a
+// ring of 4 slots by token mod 4, which unrolled rounds of 4 tokens turn into fixed
+// registers: nothing is moved.
+//
+// Measured, bf16, 4 taps, SiLU, a B200 (6568 GB/s copy): 4 x 2048 tokens x 4352
+// channels forward 36 us (3950 GB/s), backward 64 us (3340 GB/s); a token of 256
+// sequences x 10240 channels 12 us.  SiLU's two special functions an element are
+// 16 us of the forward by themselves.
 #include "ssd_internal.h"
 #include "ssd_vec.cuh"
 
@@ -104,8 +111,9 @@ __device__ __forceinline__ void load_ring(const Conv1dArgs& a, int64_t b, int64_
 
 // The forward: kFwdRound tokens' loads are in flight while the round before is
 // computed.  A run of 32 tokens reads 3 / 32 of its inputs twice and its filter
-// once per 512 bytes of input; where there are fewer threads than keep an SM's
-// loads in flight, runs of 8.
+// once for 256 (fp32: 512) bytes of input; where there are fewer threads than keep
+// an SM's loads in flight, runs of 8.  64 registers, 8 blocks an SM: 37 us at 4 x
+// 2048 x 4352, 39 us with 80 registers, 43 us with 8 channels a thread.
 constexpr int kFwdThreads = 128, kFwdRound = 4;
 
 template <typename IoT, typename YT, int W>

@@ -16,6 +16,11 @@
 // groups, so that a slot meets one group only and keeps the sums of dw and db in
 // registers.  Without the mean the backward's two sums, of c^2 and of dn c, are
 // formed at once (mean(dn nrm) = r mean(dn c)): one exchange a row.
+//
+// Measured, 8192 rows x 4096 channels, fp32 in, bf16 gate and out, a B200 (6568 GB/s
+// copy): forward 48 us (5620 GB/s), backward in 8 groups 84 us (4820 GB/s); 8 rows
+// 4 us.  Loads two rows ahead were slower (60 and 105 us against 57 and 98 us then),
+// none ahead too (66 and 133 us).
 #include "ssd_internal.h"
 #include "ssd_vec.cuh"
 

@@ -8,6 +8,11 @@
 // of tokens), so each state of each token costs one exponential and three
 // fp32 operations: with 16 states or more the scan is bound by the special
 // function units (16 results a clock and SM), below HBM's time otherwise.
+//
+// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 248 us
+// (the units alone 119 us: 63 % busy, 57 % of the issue slots, 53 % of shared
+// memory), 1 x 16384 x 2048 398 us; a token of 256 sequences x 8192 channels over
+// an fp32 state 54 us (5290 GB/s of 6568).
 #include "ssd_selective_common.cuh"
 
 namespace ssd {
@@ -384,8 +389,8 @@ static int tile_tokens(int64_t N) { return N > 128 ? 16 : 32; }
 // A block's warps each keep one of the SM's four special function units busy, two
 // blocks an SM saturate them.  Cutting the sequence costs a second exponential per
 // state and token, so it pays once four or more chunks run in the time of one:
-// from 60 blocks down (1 x 16384 tokens, 2048 channels, state 16: 32 blocks, see
-// the launch below for its times).
+// from 60 blocks down (1 x 16384 tokens, 2048 channels, state 16: 32 blocks; 6311 us
+// in one chunk by the first kernel, 398 us in 9 by this one).
 static SelShape sel_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
     SelShape sh{};
     const int CT = tile_channels(N), T = tile_tokens(N);

@@ -243,3 +243,47 @@ def test_a_workspace_given_is_used_and_nothing_behind_it_is_written():
     t.cuda.synchronize()
     assert (big[need:] == 77).all() and (big[:need] != 77).any()
     assert all(t.equal(a[k], b[k]) for k in a if a[k] is not None)
+
+
+def test_outputs_that_are_given_are_written_and_returned():
+    t = torch()
+    d = {k: to_dev(v) for k, v in selective(90).items()}
+    x, z = d["row"][..., :72], d["row"][..., 72:]
+    want, kept = ssd.conv1d_fwd(x, d["w"], d["bias"], split=(40, 32))
+    ys = (t.empty(2, 50, 40, device="cuda"), t.empty(2, 50, 32, device="cuda"))
+    final = t.empty_like(kept)
+    got, f = ssd.conv1d_fwd(x, d["w"], d["bias"], split=(40, 32), y=ys, final_state=final)
+    assert got[0] is ys[0] and got[1] is ys[1] and f is final
+    assert t.equal(ys[0], want[0]) and t.equal(ys[1], want[1]) and t.equal(final, kept)
+    assert ssd.conv1d_fwd(x, d["w"], d["bias"], want_final_state=False)[1] is None
+    y1 = t.empty(2, 72, device="cuda")
+    assert ssd.conv1d_update(kept.clone(), x[:, 0], d["w"], d["bias"], y=y1) is y1
+
+    scan = (x.contiguous(), d["dt_raw"], d["dt_bias"], d["A"], d["B"], d["C"], d["D"], z)
+    want, state = ssd.selective_scan_fwd(*scan)
+    y, final = t.empty_like(want, dtype=t.bfloat16), t.empty_like(state)
+    got, f = ssd.selective_scan_fwd(*scan, y=y, final_state=final)
+    assert got is y and f is final and t.equal(y, want.bfloat16()) and t.equal(final, state)
+    assert ssd.selective_scan_fwd(*scan, want_final_state=False)[1] is None
+    y = t.empty(2, 50, 72, device="cuda")
+    assert ssd.group_norm_fwd(want, None, None, z, ngroups=3, y=y) is y
+    assert t.equal(y, ssd.group_norm_fwd(want, None, None, z, ngroups=3))
+
+
+def test_calls_without_the_optional_gradients():
+    """dinit, the norm's weight and bias, dt_bias and D left out give the others unchanged."""
+    t = torch()
+    d = {k: to_dev(v) for k, v in selective(91).items()}
+    x, dy = d["row"][..., :72].contiguous(), to_dev(draw(92, (2, 50, 72), F))
+    a = ssd.conv1d_bwd(x, d["w"], d["bias"], dy)
+    b = ssd.conv1d_bwd(x, d["w"], d["bias"], dy, want_dinit=False)
+    assert b["dinit_state"] is None and all(t.equal(a[k], b[k]) for k in ("dx", "dweight", "dbias"))
+    zero = t.zeros(72, device="cuda")
+    a = ssd.selective_scan_bwd(x, d["dt_raw"], zero, d["A"], d["B"], d["C"], zero, dy)
+    b = ssd.selective_scan_bwd(x, d["dt_raw"], None, d["A"], d["B"], d["C"], None, dy, want_dinit=False)
+    assert b["ddt_bias"] is None and b["dD"] is None and b["dinit_state"] is None
+    assert all(t.equal(a[k], b[k]) for k in ("dx", "ddt_raw", "dA", "dB", "dC"))
+    one = t.ones(72, device="cuda")
+    a = ssd.group_norm_bwd(x, one, zero, dy, ngroups=3)
+    b = ssd.group_norm_bwd(x, None, None, dy, ngroups=3)
+    assert b["dweight"] is None and b["dbias"] is None and t.equal(a["dx"], b["dx"])
