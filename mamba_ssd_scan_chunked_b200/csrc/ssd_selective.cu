@@ -11,7 +11,7 @@
 //
 // Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 248 us
 // (the units alone 119 us: 63 % busy, 57 % of the issue slots, 53 % of shared
-// memory), 1 x 16384 x 2048 398 us; a token of 256 sequences x 8192 channels over
+// memory), 1 x 16384 x 2048 375 us; a token of 256 sequences x 8192 channels over
 // an fp32 state 54 us (5290 GB/s of 6568).
 #include "ssd_selective_common.cuh"
 
@@ -24,12 +24,13 @@ namespace ssd {
 // channels, and the block gates and stores the tile's y with whole vectors.
 //
 // Where batch and channels are too few for the machine the sequence is cut into
-// nch chunks: SUMMARY is the pass that finds the end state of every chunk but
-// the last from 0 and the sum of its dt, selective_chunks_kernel the state that
-// enters each, and the main pass starts from it.
+// nch chunks and takes two launches of nch - 1 of them: the first walks over chunk 0
+// and, for each of the others but the last, finds its end state from 0 and the sum
+// of its dt (SUMMARY); selective_chunks_kernel forms the state that enters each; the
+// second launch walks over chunks 1 to nch - 1.
 template <typename IoT, typename YT, class Tile, int T, bool SUMMARY>
-__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 8 ? 2 : 1)
-selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict__ wstate, float* __restrict__ wdt) {
+__device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const SelShape& sh, int tile, int64_t g, int64_t ck,
+                                               int64_t b, float* __restrict__ wstate, float* __restrict__ wdt) {
     constexpr int K = Tile::K, S = Tile::S, Np = Tile::Np, P = Tile::P, CT = Tile::CT, THREADS = Tile::W * 32;
     constexpr int V = CT / 8;                                   // 8-channel vectors of a token here
     constexpr int IT = (T * V + THREADS - 1) / THREADS;         // of a thread in a tile
@@ -42,16 +43,11 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
     float* sC = sB + 2 * T * Np;                                // [2][T][Np]
     float* sy = sC + (SUMMARY ? 0 : 2 * T * Np);                // [8 + T][YS]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t nch = SUMMARY ? sh.nch - 1 : sh.nch;
-    int64_t r = blockIdx.x;
-    const int tile = (int)(r % sh.tiles);
-    r /= sh.tiles;
-    const int64_t g = r % a.G;
-    r /= a.G;
-    const int64_t ck = r % nch, b = r / nch;
+    const int64_t nch = sh.nch;
     const int c0 = tile * CT, nc = sh.Dg - c0 < CT ? sh.Dg - c0 : CT;   // channels of the group here
     const int64_t d0 = g * sh.Dg + c0;
-    const int64_t tb = ck * sh.clen, te = tb + sh.clen < a.L ? tb + sh.clen : a.L;
+    const int64_t tb = ck == 0 ? 0 : sh.len0 + (ck - 1) * sh.clen, to = ck == 0 ? sh.len0 : tb + sh.clen;
+    const int64_t te = to < a.L ? to : a.L;
     int64_t p = a.pad_left ? a.pad_left[b] : 0;
     p = p < 0 ? 0 : p > a.L ? a.L : p;
 
@@ -247,34 +243,55 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
         __syncthreads();                                        // the next tile is ready, sy free
     }
     if (!cok) return;
-    const int64_t bc = b * nch + ck;
+    // what leaves a summary, or chunk 0, goes to the workspace
+    const int64_t bc = b * (nch - 1) + ck;
+    const bool keep = SUMMARY || ck < nch - 1;
     if (SUMMARY && n0 == 0) wdt[bc * a.D + d0 + ch] = sum;
-    if (!SUMMARY && !(a.final_state && ck == nch - 1)) return;
+    if (keep ? ck > 0 && !SUMMARY : !a.final_state) return;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         if (n0 + s >= a.N) continue;
         const float2 hv = f2_get(h[s / 2]);
         const float v = s & 1 ? hv.y : hv.x;
         const int64_t i = (d0 + ch) * a.N + n0 + s;
-        if (SUMMARY) wstate[bc * a.D * a.N + i] = v;
+        if (keep) wstate[bc * a.D * a.N + i] = v;
         else if (a.state_bf16) ((bf16*)a.final_state)[b * a.D * a.N + i] = from_f32<bf16>(v);
         else ((float*)a.final_state)[b * a.D * a.N + i] = v;
     }
 }
 
+template <typename IoT, typename YT, class Tile, int T, bool FIRST>
+__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 8 ? 2 : 1)
+selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict__ wstate, float* __restrict__ wdt) {
+    const int64_t here = sh.nch > 1 ? sh.nch - 1 : 1;            // chunks of this launch
+    int64_t r = blockIdx.x;
+    const int tile = (int)(r % sh.tiles);
+    r /= sh.tiles;
+    const int64_t g = r % a.G;
+    r /= a.G;
+    const int64_t ck = r % here + (FIRST || sh.nch == 1 ? 0 : 1), b = r / here;
+    if constexpr (FIRST) {
+        if (ck > 0) {
+            selective_walk<IoT, YT, Tile, T, true>(a, sh, tile, g, ck, b, wstate, wdt);
+            return;
+        }
+    }
+    selective_walk<IoT, YT, Tile, T, false>(a, sh, tile, g, ck, b, wstate, wdt);
+}
+
 // wstate[b][c]: from the end state of chunk c started at 0 to the state that
-// leaves it, c < nch - 1
+// leaves it, 0 < c < nch - 1 (chunk 0's is there)
 __global__ void __launch_bounds__(128)
 selective_chunks_kernel(const SelectiveArgs a, int nch, float* __restrict__ wstate, const float* __restrict__ wdt) {
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, DN = a.D * a.N;
     if (i >= a.batch * DN) return;
     const int64_t b = i / DN, dn = i % DN, d = dn / a.N;
     const float A2 = a.A[dn] * kLog2e;
-    float h = 0.f;
-    if (a.init) h = a.state_bf16 ? to_f32(((const bf16*)a.init)[i]) : ((const float*)a.init)[i];
     float* w = wstate + b * (nch - 1) * DN + dn;
     const float* dt = wdt + b * (nch - 1) * a.D + d;
-    for (int c = 0; c < nch - 1; ++c) {
+    float h = w[0];
+#pragma unroll 4
+    for (int c = 1; c < nch - 1; ++c) {
         h = fmaf(exp2_approx(dt[c * a.D] * A2), h, w[c * DN]);
         w[c * DN] = h;
     }
@@ -386,11 +403,11 @@ constexpr int kSelMaxChunks = 64;
 static int tile_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 static int tile_tokens(int64_t N) { return N > 128 ? 16 : 32; }
 
-// A block's warps each keep one of the SM's four special function units busy, two
-// blocks an SM saturate them.  Cutting the sequence costs a second exponential per
-// state and token, so it pays once four or more chunks run in the time of one:
-// from 60 blocks down (1 x 16384 tokens, 2048 channels, state 16: 32 blocks; 6311 us
-// in one chunk by the first kernel, 398 us in 9 by this one).
+// A block's warps keep an SM's special function units busy by half, two blocks
+// saturate them.  Cutting the sequence costs a second exponential per state and
+// token, so it pays once the two launches of nch - 1 chunks, two blocks an SM, are of
+// four chunks or more: from 98 blocks down (1 x 16384 tokens, 2048 channels, state
+// 16: 32 blocks; 6311 us in one chunk by the first kernel, in 10 by this one 375 us).
 static SelShape sel_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
     SelShape sh{};
     const int CT = tile_channels(N), T = tile_tokens(N);
@@ -398,13 +415,22 @@ static SelShape sel_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_
     sh.tiles = (sh.Dg + CT - 1) / CT;
     const int64_t blocks = batch * G * sh.tiles, ntile = (L + T - 1) / T;
     int64_t nch = 1;
-    if (blocks > 0 && blocks <= 60) nch = 296 / blocks;
+    if (blocks > 0 && blocks <= 98) nch = 296 / blocks + 1;
     if (nch > kSelMaxChunks) nch = kSelMaxChunks;
     if (nch > ntile / 2) nch = ntile / 2;
-    if (nch < 4) nch = 1;
-    const int64_t per = nch > 1 ? (ntile + nch - 1) / nch : (ntile ? ntile : 1);
+    if (nch < 4) {
+        sh.nch = 1;
+        sh.len0 = sh.clen = (int)((ntile ? ntile : 1) * T);
+        return sh;
+    }
+    // chunk 0, walked over in full while the others are summed up, has three quarters of their tiles: a
+    // summary's tile takes that much of a full one's time
+    int64_t per = (ntile + nch - 1) / nch;
+    while (3 * per / 4 + (nch - 1) * per < ntile) ++per;
+    const int64_t per0 = 3 * per / 4 > 0 ? 3 * per / 4 : 1;
+    sh.len0 = (int)(per0 * T);
     sh.clen = (int)(per * T);
-    sh.nch = (int)(nch > 1 ? (ntile + per - 1) / per : 1);
+    sh.nch = (int)(1 + (ntile - per0 + per - 1) / per);
     return sh;
 }
 
@@ -427,22 +453,22 @@ static cudaError_t launch_fwd_t(const SelectiveArgs& a, cudaStream_t s) {
     constexpr int CT = Tile::CT, Np = Tile::Np, THREADS = Tile::W * 32;
     const SelShape sh = sel_shape(a.batch, a.L, a.D, a.N, a.G);
     constexpr int YS = CT + 4;
-    constexpr int smem = (int)sizeof(float) * (T * (4 * CT + 4 * Np + YS) + 8 * YS), smem1 = (int)sizeof(float) * T * (4 * CT + 2 * Np);
+    constexpr int smem = (int)sizeof(float) * (T * (4 * CT + 4 * Np + YS) + 8 * YS);
     const auto main = selective_fwd_kernel<IoT, YT, Tile, T, false>;
-    const auto summary = selective_fwd_kernel<IoT, YT, Tile, T, true>;
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && smem1 > 48 * 1024)
-        e = cudaFuncSetAttribute(summary, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
-    if (e != cudaSuccess) return e;
+    const auto first = selective_fwd_kernel<IoT, YT, Tile, T, true>;
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     float* wstate = (float*)a.ws;
     float* wdt = (float*)(a.ws + chunk_state_bytes(a.batch, a.D, a.N, sh.nch));
-    const int64_t blocks = a.batch * a.G * sh.tiles;
+    const unsigned grid = (unsigned)(a.batch * a.G * sh.tiles * (sh.nch > 1 ? sh.nch - 1 : 1));
     if (sh.nch > 1) {
-        summary<<<(unsigned)(blocks * (sh.nch - 1)), THREADS, smem1, s>>>(a, sh, wstate, wdt);
+        first<<<grid, THREADS, smem, s>>>(a, sh, wstate, wdt);
         selective_chunks_kernel<<<(unsigned)((a.batch * a.D * a.N + 127) / 128), 128, 0, s>>>(a, sh.nch, wstate, wdt);
     }
-    main<<<(unsigned)(blocks * sh.nch), THREADS, smem, s>>>(a, sh, wstate, wdt);
+    main<<<grid, THREADS, smem, s>>>(a, sh, wstate, wdt);
     return cudaGetLastError();
 }
 

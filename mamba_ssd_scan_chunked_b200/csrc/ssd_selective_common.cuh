@@ -67,7 +67,7 @@ struct SelTile {
 
 struct SelShape {
     int Dg, tiles;           // channels of a group, blocks that cover them
-    int nch, clen;           // chunks of a sequence and their tokens
+    int nch, len0, clen;     // chunks of a sequence, tokens of chunk 0 and of the others
 };
 
 // Sums v[i] over the K lanes of a channel (xor distances P, 2 P, .. 16); lane
