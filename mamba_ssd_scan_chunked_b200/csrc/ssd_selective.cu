@@ -9,9 +9,8 @@
 // fp32 operations: with 16 states or more the scan is bound by the special
 // function units (16 results a clock and SM), below HBM's time otherwise.
 //
-// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 248 us
-// (the units alone 119 us: 63 % busy, 57 % of the issue slots, 53 % of shared
-// memory), 1 x 16384 x 2048 375 us; a token of 256 sequences x 8192 channels over
+// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 246 us
+// (the units alone 119 us), 1 x 16384 x 2048 372 us; a token of 256 sequences x 8192 channels over
 // an fp32 state 54 us (5290 GB/s of 6568).
 #include "ssd_selective_common.cuh"
 
@@ -261,7 +260,7 @@ __device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const Sel
 }
 
 template <typename IoT, typename YT, class Tile, int T, bool FIRST>
-__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 8 ? 2 : 1)
+__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 4 ? 3 : Tile::W == 8 ? 2 : 1)
 selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict__ wstate, float* __restrict__ wdt) {
     const int64_t here = sh.nch > 1 ? sh.nch - 1 : 1;            // chunks of this launch
     int64_t r = blockIdx.x;
@@ -396,18 +395,20 @@ selective_update_kernel(const SelectiveArgs a, int K, int cblocks, int Dg) {
     }
 }
 
-// Tiles by the number of states: 4 states a lane (8 beyond 128), and more warps a
-// block where a warp covers few channels, so that a token's row stays whole vectors.
+// Tiles by the number of states: 8 states a lane from 9 to 32 states and beyond 128
+// (half the loads and sums of 4 for each state: 246 against 251 us at 4 x 2048 x
+// 4096, state 16, with half the warps), 4 otherwise; more warps a block where a warp
+// covers few channels, so that a token's row stays whole vectors.
 constexpr int kSelMaxChunks = 64;
 
 static int tile_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 static int tile_tokens(int64_t N) { return N > 128 ? 16 : 32; }
 
-// A block's warps keep an SM's special function units busy by half, two blocks
-// saturate them.  Cutting the sequence costs a second exponential per state and
-// token, so it pays once the two launches of nch - 1 chunks, two blocks an SM, are of
-// four chunks or more: from 98 blocks down (1 x 16384 tokens, 2048 channels, state
-// 16: 32 blocks; 6311 us in one chunk by the first kernel, in 10 by this one 375 us).
+// Three blocks an SM saturate it.  Cutting the sequence costs a second exponential
+// per state and token, so it pays once the two launches of nch - 1 chunks are of four
+// chunks or more: from 100 blocks down (1 x 16384 tokens, 2048 channels, state 16: 32
+// blocks; 6311 us in one chunk by the first kernel, 372 us in 14 by this one; 3 x 777
+// x 520 fp32, state 24: 39 us in 9, 43 us in 6).
 static SelShape sel_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
     SelShape sh{};
     const int CT = tile_channels(N), T = tile_tokens(N);
@@ -415,7 +416,7 @@ static SelShape sel_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_
     sh.tiles = (sh.Dg + CT - 1) / CT;
     const int64_t blocks = batch * G * sh.tiles, ntile = (L + T - 1) / T;
     int64_t nch = 1;
-    if (blocks > 0 && blocks <= 98) nch = 296 / blocks + 1;
+    if (blocks > 0 && blocks <= 100) nch = 444 / blocks + 1;
     if (nch > kSelMaxChunks) nch = kSelMaxChunks;
     if (nch > ntile / 2) nch = ntile / 2;
     if (nch < 4) {
@@ -475,8 +476,8 @@ static cudaError_t launch_fwd_t(const SelectiveArgs& a, cudaStream_t s) {
 template <typename IoT, typename YT>
 static cudaError_t launch_fwd_s(const SelectiveArgs& a, cudaStream_t s) {
     if (a.N <= 8) return launch_fwd_t<IoT, YT, SelTile<2, 4, 8>, 32>(a, s);
-    if (a.N <= 16) return launch_fwd_t<IoT, YT, SelTile<4, 4, 8>, 32>(a, s);
-    if (a.N <= 32) return launch_fwd_t<IoT, YT, SelTile<8, 4, 8>, 32>(a, s);
+    if (a.N <= 16) return launch_fwd_t<IoT, YT, SelTile<2, 8, 4>, 32>(a, s);
+    if (a.N <= 32) return launch_fwd_t<IoT, YT, SelTile<4, 8, 4>, 32>(a, s);
     if (a.N <= 64) return launch_fwd_t<IoT, YT, SelTile<16, 4, 8>, 32>(a, s);
     if (a.N <= 128) return launch_fwd_t<IoT, YT, SelTile<32, 4, 16>, 32>(a, s);
     return launch_fwd_t<IoT, YT, SelTile<32, 8, 16>, 16>(a, s);
