@@ -9,7 +9,7 @@
 // fp32 operations: with 16 states or more the scan is bound by the special
 // function units (16 results a clock and SM), below HBM's time otherwise.
 //
-// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 246 us
+// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 232 us
 // (the units alone 119 us), 1 x 16384 x 2048 372 us; a token of 256 sequences x 8192 channels over
 // an fp32 state 54 us (5290 GB/s of 6568).
 #include "ssd_selective_common.cuh"
@@ -27,7 +27,7 @@ namespace ssd {
 // and, for each of the others but the last, finds its end state from 0 and the sum
 // of its dt (SUMMARY); selective_chunks_kernel forms the state that enters each; the
 // second launch walks over chunks 1 to nch - 1.
-template <typename IoT, typename YT, class Tile, int T, bool SUMMARY>
+template <typename IoT, typename YT, class Tile, int T, bool SUMMARY, bool DEEP>
 __device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const SelShape& sh, int tile, int64_t g, int64_t ck,
                                                int64_t b, float* __restrict__ wstate, float* __restrict__ wdt) {
     constexpr int K = Tile::K, S = Tile::S, Np = Tile::Np, P = Tile::P, CT = Tile::CT, THREADS = Tile::W * 32;
@@ -188,6 +188,7 @@ __device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const Sel
 #pragma unroll
             for (int i = 0; i < (K >= 8 ? 1 : 8 / K); ++i) out[i * YS] = y[i];
         };
+#pragma unroll DEEP ? 2 : 1
         for (int t = 0; t < nt; t += 8) {
             float yn[8];
 #pragma unroll
@@ -259,8 +260,10 @@ __device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const Sel
     }
 }
 
-template <typename IoT, typename YT, class Tile, int T, bool FIRST>
-__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 4 ? 3 : Tile::W == 8 ? 2 : 1)
+// DEEP: for blocks of 4 warps of which an SM has two at most, registers for two
+// rounds side by side (4 x 2048 x 4096: 246 -> 232 us; three blocks an SM lose by it)
+template <typename IoT, typename YT, class Tile, int T, bool FIRST, bool DEEP>
+__global__ void __launch_bounds__(Tile::W * 32, Tile::W == 4 && !DEEP ? 3 : Tile::W <= 8 ? 2 : 1)
 selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict__ wstate, float* __restrict__ wdt) {
     const int64_t here = sh.nch > 1 ? sh.nch - 1 : 1;            // chunks of this launch
     int64_t r = blockIdx.x;
@@ -271,11 +274,11 @@ selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict
     const int64_t ck = r % here + (FIRST || sh.nch == 1 ? 0 : 1), b = r / here;
     if constexpr (FIRST) {
         if (ck > 0) {
-            selective_walk<IoT, YT, Tile, T, true>(a, sh, tile, g, ck, b, wstate, wdt);
+            selective_walk<IoT, YT, Tile, T, true, DEEP>(a, sh, tile, g, ck, b, wstate, wdt);
             return;
         }
     }
-    selective_walk<IoT, YT, Tile, T, false>(a, sh, tile, g, ck, b, wstate, wdt);
+    selective_walk<IoT, YT, Tile, T, false, DEEP>(a, sh, tile, g, ck, b, wstate, wdt);
 }
 
 // wstate[b][c]: from the end state of chunk c started at 0 to the state that
@@ -455,8 +458,11 @@ static cudaError_t launch_fwd_t(const SelectiveArgs& a, cudaStream_t s) {
     const SelShape sh = sel_shape(a.batch, a.L, a.D, a.N, a.G);
     constexpr int YS = CT + 4;
     constexpr int smem = (int)sizeof(float) * (T * (4 * CT + 4 * Np + YS) + 8 * YS);
-    const auto main = selective_fwd_kernel<IoT, YT, Tile, T, false>;
-    const auto first = selective_fwd_kernel<IoT, YT, Tile, T, true>;
+    const unsigned grid = (unsigned)(a.batch * a.G * sh.tiles * (sh.nch > 1 ? sh.nch - 1 : 1));
+    const bool deep = Tile::W == 4 && sh.nch == 1 && grid <= 296;
+    const auto main = deep ? selective_fwd_kernel<IoT, YT, Tile, T, false, Tile::W == 4>
+                           : selective_fwd_kernel<IoT, YT, Tile, T, false, false>;
+    const auto first = selective_fwd_kernel<IoT, YT, Tile, T, true, false>;
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -464,7 +470,6 @@ static cudaError_t launch_fwd_t(const SelectiveArgs& a, cudaStream_t s) {
     }
     float* wstate = (float*)a.ws;
     float* wdt = (float*)(a.ws + chunk_state_bytes(a.batch, a.D, a.N, sh.nch));
-    const unsigned grid = (unsigned)(a.batch * a.G * sh.tiles * (sh.nch > 1 ? sh.nch - 1 : 1));
     if (sh.nch > 1) {
         first<<<grid, THREADS, smem, s>>>(a, sh, wstate, wdt);
         selective_chunks_kernel<<<(unsigned)((a.batch * a.D * a.N + 127) / 128), 128, 0, s>>>(a, sh.nch, wstate, wdt);

@@ -49,6 +49,8 @@ def args(d):
     (1, 2100, 40, 40, 1, B, F, F, True, True, True, None, 0),
     (4, 50, 40, 16, 1, F, F, F, True, True, True, [0, 1, 49, 50], 0),
     (3, 700, 24, 16, 1, F, B, F, False, True, True, [699, 64, -1], 8),
+    (75, 20, 264, 16, 1, B, B, F, True, True, True, None, 8),            # more blocks than two for every SM
+    (80, 9, 136, 24, 1, F, F, F, True, False, True, None, 0),
     (2, 1, 16, 16, 1, B, B, B, True, True, True, None, 0),
     (2, 0, 16, 16, 1, F, F, F, True, True, True, None, 0),
     (0, 4, 16, 16, 1, F, F, F, False, False, True, None, 0),
