@@ -9,9 +9,9 @@
 // fp32 operations: with 16 states or more the scan is bound by the special
 // function units (16 results a clock and SM), below HBM's time otherwise.
 //
-// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 232 us
-// (the units alone 119 us), 1 x 16384 x 2048 372 us; a token of 256 sequences x 8192 channels over
-// an fp32 state 54 us (5290 GB/s of 6568).
+// Measured, bf16, gated, state 16, a B200: 4 x 2048 tokens x 4096 channels 234 us
+// (the states' exponentials alone 119 us), 1 x 16384 x 2048 374 us; a token of
+// 256 sequences x 8192 channels over an fp32 state 54 us (5290 GB/s of 6568).
 #include "ssd_selective_common.cuh"
 
 namespace ssd {
