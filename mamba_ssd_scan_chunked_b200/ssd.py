@@ -13,6 +13,11 @@ as are those of the operators around the scan (``conv1d_fwd``, ``conv1d_update``
 ``selective_scan_bwd``, ``group_norm_fwd``, ``group_norm_bwd``).  These work on
 the device of their tensors and, unless ``stream`` is given, on its current
 stream; outputs and workspaces that they allocate belong to the launching stream.
+A given ``stream`` first waits for the current one, so that tensors made there may
+be passed, and dropped after the call; to leave the two apart make it the current
+one (``torch.cuda.stream``).  What a call wrote is read elsewhere after the caller's
+own wait for that stream.  Where a graph captures one of the two streams alone there
+is no wait, and the tensors are the caller's to keep.
 """
 from __future__ import annotations
 
@@ -790,9 +795,11 @@ def _one_device(dense, rows=()) -> int:
     return index
 
 
-def _launch_on(index, stream, call):
+def _launch_on(index, stream, call, tensors=()):
     """``call(handle)`` with device ``index`` the current one and ``stream`` (None: the device's current
-    stream) the one that outputs and workspaces are allocated for and the call is enqueued on."""
+    stream) the one that outputs and workspaces are allocated for and the call is enqueued on.  A stream
+    other than the current one waits for the current one first, and ``tensors`` (the caller's; None passes)
+    keep their memory until it has used them."""
     import torch
     if stream is None:
         if index == torch.cuda.current_device():
@@ -803,8 +810,17 @@ def _launch_on(index, stream, call):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
     if stream.device.index != index:
         raise ValueError(f"stream on device {stream.device.index}, tensors on device {index}")
-    with torch.cuda.device(index), torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+    with torch.cuda.device(index):
+        current = torch.cuda.current_stream(index)
+        captured = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(stream):
+            # a graph that captures one of the two streams alone cannot hold the wait
+            if stream.cuda_stream != current.cuda_stream and torch.cuda.is_current_stream_capturing() == captured:
+                stream.wait_stream(current)
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+            return call(stream.cuda_stream)
 
 
 def _workspace(workspace, need, x):
@@ -888,7 +904,8 @@ def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation=
     _check(pad_left, (b,), "pad_left", torch.int32)
     out = _conv_outputs(y, widths, (b, L), y_dtype, split is None) if y is not None else ()
     desc = _conv_desc(b, L, D, W, xs, D, widths, x.dtype, y_dtype, state_dtype, activation)
-    device = _one_device((weight, bias, init_state, pad_left, final_state, *out), (x,))
+    dense, rows = (weight, bias, init_state, pad_left, final_state, *out), (x,)
+    device = _one_device(dense, rows)
 
     def call(handle):
         ys = out if y is not None else [x.new_empty((b, L, n), dtype=y_dtype) for n in widths]
@@ -901,7 +918,7 @@ def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation=
             raise SsdError(st, "ssd_conv1d_fwd")
         return (ys[0] if split is None else tuple(ys)), final
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu", y=None, y_dtype=None, stream=None):
@@ -919,7 +936,8 @@ def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu",
     _check(state, (b, W - 1, D), "state")
     out = _conv_outputs(y, widths, (b,), y_dtype, split is None) if y is not None else ()
     desc = _conv_desc(b, 1, D, W, xs, D, widths, x.dtype, y_dtype, state.dtype, activation)
-    device = _one_device((state, weight, bias, *out), (x,))
+    dense, rows = (state, weight, bias, *out), (x,)
+    device = _one_device(dense, rows)
 
     def call(handle):
         ys = out if y is not None else [x.new_empty((b, n), dtype=y_dtype) for n in widths]
@@ -928,7 +946,7 @@ def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu",
             raise SsdError(st, "ssd_conv1d_update")
         return ys[0] if split is None else tuple(ys)
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activation="silu", dx=None,
@@ -960,7 +978,8 @@ def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activ
     for t, n in zip(dys, widths):
         _check(t, (b, L, n), "dy", x.dtype)
     desc = _conv_desc(b, L, D, W, xs, dxs, widths, x.dtype, grad_dtype, state_dtype, activation)
-    device = _one_device((weight, bias, init_state, dfinal_state, workspace, *dys), (x, dx))
+    dense, rows = (weight, bias, init_state, dfinal_state, workspace, *dys), (x, dx)
+    device = _one_device(dense, rows)
     need = ssd_conv1d_bwd_workspace_size(desc)
 
     def call(handle):
@@ -977,7 +996,7 @@ def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activ
             raise SsdError(st, "ssd_conv1d_bwd")
         return out
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def _selective_args(lead, x, dt_raw, dt_bias, A, B, C, D, z, y_dtype, state_dtype) -> SelectiveDesc:
@@ -1020,7 +1039,8 @@ def selective_scan_fwd(x, dt_raw, dt_bias, A, B, C, D, z=None, init_state=None, 
     _check(final_state, states, "final_state", state_dtype)
     _check(y, (b, L, ch), "y", y_dtype)
     _check(pad_left, (b,), "pad_left", torch.int32)
-    device = _one_device((x, dt_raw, dt_bias, A, B, C, D, init_state, pad_left, y, final_state, workspace), (z,))
+    dense, rows = (x, dt_raw, dt_bias, A, B, C, D, init_state, pad_left, y, final_state, workspace), (z,)
+    device = _one_device(dense, rows)
     need = ssd_selective_scan_workspace_size(desc)
 
     def call(handle):
@@ -1036,7 +1056,7 @@ def selective_scan_fwd(x, dt_raw, dt_bias, A, B, C, D, z=None, init_state=None, 
             raise SsdError(st, "ssd_selective_scan_fwd")
         return out, final
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=None, y_dtype=None, stream=None):
@@ -1049,7 +1069,8 @@ def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=N
     desc = _selective_args((b,), x, dt_raw, dt_bias, A, B, C, D, z, y_dtype, state.dtype)
     _check(state, (b, ch, B.shape[-1]), "state")
     _check(y, (b, ch), "y", y_dtype)
-    device = _one_device((state, x, dt_raw, dt_bias, A, B, C, D, y), (z,))
+    dense, rows = (state, x, dt_raw, dt_bias, A, B, C, D, y), (z,)
+    device = _one_device(dense, rows)
 
     def call(handle):
         out = x.new_empty((b, ch), dtype=y_dtype) if y is None else y
@@ -1060,7 +1081,7 @@ def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=N
             raise SsdError(st, "ssd_selective_state_update")
         return out
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=None, dfinal_state=None, *,
@@ -1084,7 +1105,8 @@ def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=No
     _check(dy, (b, L, ch), "dy", x.dtype)
     _check(init_state, states, "init_state", state_dtype)
     _check(dfinal_state, states, "dfinal_state", state_dtype)
-    device = _one_device((x, dt_raw, dt_bias, A, B, C, D, dy, init_state, dfinal_state, workspace), (z,))
+    dense, rows = (x, dt_raw, dt_bias, A, B, C, D, dy, init_state, dfinal_state, workspace), (z,)
+    device = _one_device(dense, rows)
     need = ssd_selective_scan_bwd_workspace_size(desc)
 
     def call(handle):
@@ -1108,7 +1130,7 @@ def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=No
             raise SsdError(st, "ssd_selective_scan_bwd")
         return out
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype) -> GroupNormDesc:
@@ -1143,7 +1165,8 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, ce
         y_dtype = y.dtype if y is not None else io_dtype
     desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype)
     _check(y, x.shape, "y", y_dtype)
-    device = _one_device((x, weight, bias, y), (z,))
+    dense, rows = (x, weight, bias, y), (z,)
+    device = _one_device(dense, rows)
 
     def call(handle):
         out = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
@@ -1152,7 +1175,7 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, ce
             raise SsdError(st, "ssd_group_norm_fwd")
         return out
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))
 
 
 def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=False, gate_first=True,
@@ -1164,7 +1187,8 @@ def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=F
         grad_dtype = dy.dtype
     desc = _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, dy.dtype, grad_dtype)
     _check(dy, x.shape, "dy")
-    device = _one_device((x, weight, bias, dy, workspace), (z,))
+    dense, rows = (x, weight, bias, dy, workspace), (z,)
+    device = _one_device(dense, rows)
     need = ssd_group_norm_bwd_workspace_size(desc)
 
     def call(handle):
@@ -1181,4 +1205,4 @@ def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=F
             raise SsdError(st, "ssd_group_norm_bwd")
         return out
 
-    return _launch_on(device, stream, call)
+    return _launch_on(device, stream, call, (*dense, *rows))

@@ -319,3 +319,79 @@ def test_the_stream_of_another_device_is_refused(monkeypatch):
 
     with pytest.raises(ValueError, match="stream on device 1"):
         ssd._launch_on(0, Stream(), lambda handle: handle)
+
+
+@pytest.mark.parametrize("captures", [(), ("main", "side"), ("side",), ("main",)])
+def test_a_given_stream_waits_for_the_current_one_and_its_tensors_are_kept(monkeypatch, captures):
+    """The inputs may be made on the current stream just before the call and dropped just after it: the
+    given stream waits for the current one, and the allocator learns of the use.  A capture that one of the
+    two alone takes part in cannot hold the wait."""
+    events = []
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+        def __init__(self, name, handle):
+            self.name, self.cuda_stream = name, handle
+
+        def wait_stream(self, other):
+            events.append((self.name, "waits for", other.name))
+
+    class Tensor:
+        def record_stream(self, stream):
+            events.append(("kept for", stream.name))
+
+    class Inside:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            now.append(self.stream)
+
+        def __exit__(self, *_):
+            now.pop()
+
+    main, side = Stream("main", 0), Stream("side", 64)
+    now = [main]
+    monkeypatch.setattr(torch.cuda, "device", lambda index: Inside(now[-1]))
+    monkeypatch.setattr(torch.cuda, "stream", Inside)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: now[-1])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[-1].name in captures)
+    call = lambda handle: events.append(("launched on", handle)) or now[-1].name
+
+    assert ssd._launch_on(0, side, call, (Tensor(), None, Tensor())) == "side"
+    kept = [("side", "waits for", "main"), ("kept for", "side"), ("kept for", "side")]
+    assert events == (kept if len(captures) != 1 else []) + [("launched on", 64)]
+    events.clear()
+    assert ssd._launch_on(0, main, call, (Tensor(),)) == "main"       # the current stream itself
+    assert events == [("launched on", 0)]
+
+
+def test_calls_hand_over_every_tensor_they_use(monkeypatch):
+    """What a call reads and writes among the caller's tensors is what a given stream has to keep."""
+    seen = []
+    monkeypatch.setattr(ssd, "_one_device", lambda dense, rows=(): 0)
+    monkeypatch.setattr(ssd, "_launch_on", lambda index, stream, call, tensors=(): seen.append(tensors))
+    z = lambda *shape: torch.zeros(shape)
+    D, N = 16, 8
+    io, tok, bc, tbc = (2, 5, D), (2, D), (2, 5, 1, N), (2, 1, N)
+    i32 = torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    par = [z(D), z(D, N)]                                             # dt_bias, A
+
+    def same(call, *tensors, **named):
+        call(*tensors, **named)
+        given = [t for t in (*tensors, *named.values()) for t in (t if isinstance(t, tuple) else (t,))]
+        assert {id(t) for t in seen.pop() if t is not None} == {id(t) for t in given if torch.is_tensor(t)}, call
+
+    same(ssd.conv1d_fwd, z(*io), z(D, 4), z(D), z(2, 3, D), split=(8, 8), pad_left=i32, y=(z(2, 5, 8), z(2, 5, 8)),
+         final_state=z(2, 3, D))
+    same(ssd.conv1d_update, z(2, 3, D), z(*tok), z(D, 4), z(D), y=z(*tok))
+    same(ssd.conv1d_bwd, z(*io), z(D, 4), z(D), (z(2, 5, 8), z(2, 5, 8)), z(2, 3, D), z(2, 3, D), dx=z(*io), workspace=ws)
+    same(ssd.selective_scan_fwd, z(*io), z(*io), *par, z(*bc), z(*bc), z(D), z(*io), z(2, D, N), y=z(*io),
+         final_state=z(2, D, N), pad_left=i32, workspace=ws)
+    same(ssd.selective_state_update, z(2, D, N), z(*tok), z(*tok), *par, z(*tbc), z(*tbc), z(D), z(*tok), y=z(*tok))
+    same(ssd.selective_scan_bwd, z(*io), z(*io), *par, z(*bc), z(*bc), z(D), z(*io), z(*io), z(2, D, N), z(2, D, N),
+         workspace=ws)
+    same(ssd.group_norm_fwd, z(*io), z(D), z(D), z(*io), y=z(*io))
+    same(ssd.group_norm_bwd, z(*io), z(D), z(D), z(*io), z(*io), workspace=ws)

@@ -231,6 +231,28 @@ def test_stream_argument_owns_what_the_call_allocates():
             assert t.equal(got[k], want[k]) and t.equal(raw[k], want[k]), k
 
 
+def test_a_given_stream_waits_for_inputs_made_just_before_and_keeps_them():
+    """The inputs are written behind 20 ms of other work of the current stream and dropped after the call:
+    the given stream reads what that work made, not what lay there before, and no later tensor of the
+    current stream gets their memory while it reads."""
+    t = torch()
+    d = {k: to_dev(v) for k, v in selective(72, 2, 400, 264).items()}
+    z = d["row"][..., 264:]
+    par = [d["dt_bias"], d["A"], d["B"], d["C"], d["D"]]
+    want = ssd.selective_scan_fwd(d["row"][..., :264].contiguous(), d["dt_raw"], *par, z)
+    for s in (t.cuda.Stream(), t.cuda.Stream().cuda_stream):
+        t.cuda.synchronize()
+        t.cuda._sleep(40_000_000)
+        x = d["row"][..., :264].contiguous()
+        dt = d["dt_raw"] + 0.0
+        got = ssd.selective_scan_fwd(x, dt, *par, z, stream=s)
+        del x, dt
+        junk = [t.full((2, 400, 264), float("nan"), device="cuda") for _ in range(8)]
+        t.cuda.synchronize()
+        del junk
+        assert t.equal(got[0], want[0]) and t.equal(got[1], want[1])
+
+
 def test_a_workspace_given_is_used_and_nothing_behind_it_is_written():
     t = torch()
     d = {k: to_dev(v) for k, v in selective(80).items()}
