@@ -63,7 +63,7 @@ __device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const Sel
             const int s = 2 * s2 + q;
             const int64_t i = (d0 + ch) * a.N + n0 + s;
             if (cok && n0 + s < a.N) {
-                Av[q] = a.A[i] * kLog2e;
+                Av[q] = decay_rate(a.A[i]);
                 const int64_t k = b * a.D * a.N + i;
                 if (SUMMARY) continue;
                 if (ck > 0) hv[q] = wstate[(b * (nch - 1) + ck - 1) * a.D * a.N + i];
@@ -288,7 +288,7 @@ selective_chunks_kernel(const SelectiveArgs a, int nch, float* __restrict__ wsta
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, DN = a.D * a.N;
     if (i >= a.batch * DN) return;
     const int64_t b = i / DN, dn = i % DN, d = dn / a.N;
-    const float A2 = a.A[dn] * kLog2e;
+    const float A2 = decay_rate(a.A[dn]);
     float* w = wstate + b * (nch - 1) * DN + dn;
     const float* dt = wdt + b * (nch - 1) * a.D + d;
     float h = w[0];
@@ -361,7 +361,7 @@ selective_update_kernel(const SelectiveArgs a, int K, int cblocks, int Dg) {
             for (int s = 0; s < VS; s += 4) {
                 Vec16<float>::load(a.A + (int64_t)d * N + n + s, A2[r] + s);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) A2[r][s + q] *= kLog2e;
+                for (int q = 0; q < 4; ++q) A2[r][s + q] = decay_rate(A2[r][s + q]);
             }
     }
     const float dt = f2_get(softplus2(raw + bias, raw + bias)).x, dx = dt * x;

@@ -162,9 +162,12 @@ __device__ __forceinline__ void store_states(float* p, int64_t i, int64_t N, int
         if (n0 + s < N) *reinterpret_cast<ulonglong2*>(p + i * N + n0 + s) = make_ulonglong2(v[s / 2], v[s / 2 + 1]);
 }
 template <int S>
-__device__ __forceinline__ void times_log2e(f32x2 (&v)[S / 2]) {
+__device__ __forceinline__ void decay_rates(f32x2 (&v)[S / 2]) {
 #pragma unroll
-    for (int s = 0; s < S / 2; ++s) v[s] = f2_mul(v[s], f2_pack(kLog2e, kLog2e));
+    for (int s = 0; s < S / 2; ++s) {
+        const float2 A = f2_get(v[s]);
+        v[s] = f2_pack(decay_rate(A.x), decay_rate(A.y));
+    }
 }
 
 // Step 1.
@@ -193,7 +196,7 @@ selective_bwd_summary_kernel(const SelectiveArgs a, const SbShape sh) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         load_states<S>(a.A, d0 + ch + e, a.N, n0, ok, A2[e]);
-        times_log2e<S>(A2[e]);
+        decay_rates<S>(A2[e]);
 #pragma unroll
         for (int s = 0; s < S / 2; ++s) {
             h[e][s] = Gs[e][s] = 0;
@@ -261,7 +264,7 @@ selective_bwd_chunks_kernel(const SelectiveArgs a, const SbShape sh, int half) {
     const int64_t i = (int64_t)(blockIdx.x - (back ? half : 0)) * 128 + threadIdx.x, DN = a.D * a.N;
     if (i >= a.batch * DN) return;
     const int64_t b = i / DN, dn = i % DN, d = dn / a.N;
-    const float A2 = a.A[dn] * kLog2e;
+    const float A2 = decay_rate(a.A[dn]);
     float* w = (float*)(a.ws + (back ? sh.off_g : sh.off_h)) + b * sh.nch * DN + dn;
     const float* wdt = (const float*)(a.ws + sh.off_dt) + b * sh.nch * a.D + d;
     const void* from = back ? a.dfinal : a.init;
@@ -372,7 +375,7 @@ selective_bwd_main_kernel(const SelectiveArgs a, const SbShape sh) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             load_states<S>(a.A, d0 + ch + e, a.N, n0, ok, A2[e]);
-            times_log2e<S>(A2[e]);
+            decay_rates<S>(A2[e]);
             load_states<S>(wh, bc * a.D + d0 + ch + e, a.N, n0, ok, h[e]);
             load_states<S>(wg, bc * a.D + d0 + ch + e, a.N, n0, ok, w[e]);
 #pragma unroll

@@ -14,6 +14,13 @@ __device__ __forceinline__ f32x2 f2_exp2(f32x2 v) {
     const float2 t = f2_get(v);
     return f2_pack(exp2_approx(t.x), exp2_approx(t.y));
 }
+// A log2 e, what exp2(dt . ) takes, with the lowest fp32 value in the place of -inf (a
+// state that forgets at once): absent tokens and padding have dt = 0, and 0 times
+// infinity is NaN where the decay is 1.  NaN stays.
+__device__ __forceinline__ float decay_rate(float A) {
+    const float v = A * kLog2e;
+    return v < -3.402823466e38f ? -3.402823466e38f : v;
+}
 // S consecutive floats (16-byte aligned) as S / 2 pairs
 template <int S> __device__ __forceinline__ void f2_load(const float* p, f32x2 (&v)[S / 2]) {
 #pragma unroll

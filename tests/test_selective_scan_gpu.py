@@ -186,3 +186,36 @@ def test_gradients_against_differences_of_the_forward_kernel():
         down, _ = loss({**d, k: d[k] - h * step})
         num, ana = (up - down) / (2 * h), float((grads[k].double() * step).sum())
         assert abs(num - ana) <= 2.0 ** -9 * (size + abs(ana)), (k, num, ana, size)
+
+
+@pytest.mark.parametrize("L,N,pad", [(13, 16, None), (13, 16, [5, 13]), (70, 24, [0, 33]), (900, 16, [0, 450])])
+def test_a_state_that_forgets_at_once(L, N, pad):
+    """A = -inf, which -exp(a) of a large a is: the state holds its own token's term alone.  Tokens that are
+    absent, before the sequence or behind its end in a tile, leave it as it was (dt = 0, decay 1, not 0 x inf);
+    so does the sum of dt of a chunk without tokens.  d dt takes A itself, which gives no number there."""
+    t = torch()
+    c = case(2, L, 24, N, 1, F, F, True, True, True, 31 + L)
+    c["A"][:, 2] = -np.inf
+    c["A"][::3, 5] = -3e38                                    # finite, and infinite times log2 e
+    d, f = on_gpu(c), {k: f64(v) for k, v in c.items()}
+    pads = None if pad is None else t.tensor(pad, dtype=t.int32, device="cuda")
+    got, final = ssd.selective_scan_fwd(*args(d), d["z"], d["init"], pad_left=pads)
+    ref, fref = O.selective_scan(*args(f), f["z"], f["init"], pad)
+    check("y", got, ref)
+    check("final", final, fref)
+    if pad is None:
+        dy = draw([33, L], (2, L, 24), F)
+        g = ssd.selective_scan_bwd(*args(d), to_dev(dy), d["z"], d["init"])
+        with np.errstate(invalid="ignore"):
+            ref = O.selective_scan_bwd(*args(f), f["z"], f["init"], f64(dy))
+        for k in ("dx", "dz", "dB", "dC", "dA", "dD", "dinit_state"):
+            check(k, g[k], ref[k])
+
+
+def test_a_token_step_of_a_state_that_forgets_at_once():
+    c = case(3, None, 24, 16, 1, F, F, True, True, True, 32)
+    c["A"][:, 2] = -np.inf
+    d, f = on_gpu(c), {k: f64(v) for k, v in c.items()}
+    h, y = O.selective_step(f["init"], f["x"], f["dt_raw"], f["dt_bias"], f["A"], f["B"], f["C"], f["D"], f["z"])
+    check("y", ssd.selective_state_update(d["init"], *args(d), d["z"]), y)
+    check("state", d["init"], h)
