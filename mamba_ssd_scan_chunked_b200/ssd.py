@@ -918,7 +918,7 @@ def conv1d_fwd(x, weight, bias=None, init_state=None, *, split=None, activation=
             raise SsdError(st, "ssd_conv1d_fwd")
         return (ys[0] if split is None else tuple(ys)), final
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu", y=None, y_dtype=None, stream=None):
@@ -946,7 +946,7 @@ def conv1d_update(state, x, weight, bias=None, *, split=None, activation="silu",
             raise SsdError(st, "ssd_conv1d_update")
         return ys[0] if split is None else tuple(ys)
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activation="silu", dx=None,
@@ -996,7 +996,7 @@ def conv1d_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, *, activ
             raise SsdError(st, "ssd_conv1d_bwd")
         return out
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def _selective_args(lead, x, dt_raw, dt_bias, A, B, C, D, z, y_dtype, state_dtype) -> SelectiveDesc:
@@ -1056,7 +1056,7 @@ def selective_scan_fwd(x, dt_raw, dt_bias, A, B, C, D, z=None, init_state=None, 
             raise SsdError(st, "ssd_selective_scan_fwd")
         return out, final
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=None, y_dtype=None, stream=None):
@@ -1081,7 +1081,7 @@ def selective_state_update(state, x, dt_raw, dt_bias, A, B, C, D, z=None, *, y=N
             raise SsdError(st, "ssd_selective_state_update")
         return out
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=None, dfinal_state=None, *,
@@ -1130,7 +1130,7 @@ def selective_scan_bwd(x, dt_raw, dt_bias, A, B, C, D, dy, z=None, init_state=No
             raise SsdError(st, "ssd_selective_scan_bwd")
         return out
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def _norm_desc(x, z, weight, bias, ngroups, eps, center, gate_first, activation, io_dtype, y_dtype) -> GroupNormDesc:
@@ -1175,7 +1175,7 @@ def group_norm_fwd(x, weight=None, bias=None, z=None, *, ngroups=1, eps=1e-5, ce
             raise SsdError(st, "ssd_group_norm_fwd")
         return out
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))
 
 
 def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=False, gate_first=True,
@@ -1205,4 +1205,4 @@ def group_norm_bwd(x, weight, bias, dy, z=None, *, ngroups=1, eps=1e-5, center=F
             raise SsdError(st, "ssd_group_norm_bwd")
         return out
 
-    return _launch_on(device, stream, call, (*dense, *rows))
+    return _launch_on(device, stream, call, () if stream is None else (*dense, *rows))

@@ -380,7 +380,7 @@ def test_calls_hand_over_every_tensor_they_use(monkeypatch):
     par = [z(D), z(D, N)]                                             # dt_bias, A
 
     def same(call, *tensors, **named):
-        call(*tensors, **named)
+        call(*tensors, **named, stream=object())
         given = [t for t in (*tensors, *named.values()) for t in (t if isinstance(t, tuple) else (t,))]
         assert {id(t) for t in seen.pop() if t is not None} == {id(t) for t in given if torch.is_tensor(t)}, call
 
