@@ -12,10 +12,11 @@
 // expanded form, which cancels).  Items, the pairs (row, group) in memory order,
 // go to slots of `lanes` neighbouring threads, each with NV vectors of 8
 // channels: part of a warp, or several warps.  A slot's next item is loaded
-// while its present one is summed.  The number of slots is a multiple of the
-// groups, so that a slot meets one group only and keeps the sums of dw and db in
-// registers.  Without the mean the backward's two sums, of c^2 and of dn c, are
-// formed at once (mean(dn nrm) = r mean(dn c)): one exchange a row.
+// while its present one is summed.  Where a slot has more than one item the
+// number of slots is a multiple of the groups, so that a slot meets one group only
+// and keeps the sums of dw and db in registers.  Without the mean the backward's two
+// sums, of c^2 and of dn c, are formed at once (mean(dn nrm) = r mean(dn c)): one
+// exchange a row.
 //
 // Measured, 8192 rows x 4096 channels, fp32 in, bf16 gate and out, a B200 (6568 GB/s
 // copy): forward 48 us (5620 GB/s), backward in 8 groups 84 us (4820 GB/s); 8 rows
@@ -39,6 +40,7 @@ struct NormShape {
     int threads;     // of a block
     int per_block;   // slots of a block
     int64_t blocks, items;
+    int64_t parts;   // rows of the backward's partial sums
 };
 
 // Where a thread stands, and its way through the sums over its slot: within a
@@ -369,9 +371,10 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
         dxp += xstep;
         dzp += xstep;
     }
-    // slot q's sums: row q / G of [slots / G][C]
+    // slot q's sums: row q / G of [parts][C]
+    if (at.first >= sh.items) return;
     float* part = a.ws + at.first * sh.gs;
-    const int64_t all = at.step * sh.gs;
+    const int64_t all = sh.parts * a.C;
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
         const int i = (at.lane + q * sh.lanes) * 8;
@@ -412,22 +415,24 @@ static NormShape norm_shape(int64_t rows, int64_t C, int64_t G, bool backward, N
         sh.threads = sh.lanes * sh.per_block;
     }
     sh.items = rows * G;
-    // blocks: a multiple of `unit`, so that all slots together are a multiple of G; as many as fit on the
-    // machine at once, so that each keeps its next item's loads in flight
+    // blocks: one item a slot where that is few; else a multiple of `unit`, so that all slots together are
+    // a multiple of G, and as many as fit on the machine at once, so that each keeps its next item's loads in
+    // flight (fewer than `want` of them: every slot has an item)
     int64_t x = G, y = sh.per_block;
     while (y) { const int64_t m = x % y; x = y; y = m; }
     const int64_t unit = G / x, want = (sh.items + sh.per_block - 1) / sh.per_block;
     const bool half = *cls == NormClass::kBlock512 || (backward && *cls == NormClass::kBlock1024);
     const int64_t most = (int64_t)148 * norm_blocks_per_sm(backward, *cls == NormClass::kWarp ? 256 : half ? 512 : 1024);
-    const int64_t n = want < most ? want : most / unit > 0 ? most / unit * unit : unit;
-    sh.blocks = (n + unit - 1) / unit * unit;
+    const bool single = want < most || want <= unit;
+    sh.blocks = single ? want : most / unit > 0 ? most / unit * unit : unit;
+    sh.parts = single ? rows : sh.blocks * sh.per_block / G;
     return sh;
 }
 
 size_t group_norm_bwd_workspace(int64_t rows, int64_t C, int64_t G) {
     NormClass cls;
     const NormShape sh = norm_shape(rows, C, G, true, &cls);
-    return rows ? (size_t)sh.blocks * sh.per_block * sh.gs * 2 * sizeof(float) : 0;
+    return (size_t)sh.parts * C * 2 * sizeof(float);
 }
 
 template <typename X, typename I, typename Y> struct NormFwd {
@@ -478,9 +483,8 @@ cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s) {
     dispatch_types<NormBwd>(a, sh, cls, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!a.dw && !a.db)) return e;
-    const int64_t rows = sh.blocks * sh.per_block / a.G;
-    const ColumnSum sums[] = {{a.ws, rows, a.C, a.dw ? a.C : 0, a.dw, a.C, nullptr, false},
-                              {a.ws + rows * a.C, rows, a.C, a.db ? a.C : 0, a.db, a.C, nullptr, false}};
+    const ColumnSum sums[] = {{a.ws, sh.parts, a.C, a.dw ? a.C : 0, a.dw, a.C, nullptr, false},
+                              {a.ws + sh.parts * a.C, sh.parts, a.C, a.db ? a.C : 0, a.db, a.C, nullptr, false}};
     return launch_column_sums(sums, 2, s);
 }
 

@@ -102,3 +102,22 @@ def test_group_norm_bwd_repeats_bit_for_bit():
     outs = [ssd.group_norm_bwd(dev(c["x"]), dev(c["weight"]), dev(c["bias"]), dy, z, ngroups=4) for _ in range(2)]
     for k in outs[0]:
         assert t.equal(outs[0][k], outs[1][k]), k
+
+
+@pytest.mark.parametrize("rows,gs,G,center,act", [(1, 8, 2047, False, "before"), (3, 16, 4099, True, "after"),
+                                                  (2, 8, 7, False, "none"), (5, 264, 601, False, "before")])
+def test_few_rows_of_many_groups(rows, gs, G, center, act):
+    """An item a slot, slots of the last block without one, and as many groups as share no factor with a block's
+    slots; the workspace is of the size asked for and nothing behind it is written."""
+    t = torch()
+    c = inputs(rows, gs * G, F, F, act, True, True, 900 + G)
+    dy, z = draw([9, G], (rows, gs * G), F), dev(c["z"])
+    got = ssd.group_norm_fwd(dev(c["x"]), dev(c["weight"]), dev(c["bias"]), z, **kw(act, G, center))
+    check("y", got, O.group_norm(f64(c["x"]), f64(c["weight"]), f64(c["bias"]), f64(c["z"]), G, 1e-5, center, act))
+    need = 2 * 4 * rows * gs * G
+    ws = t.full((need + 4096,), 77, dtype=t.uint8, device="cuda")
+    got = ssd.group_norm_bwd(dev(c["x"]), dev(c["weight"]), dev(c["bias"]), to_dev(dy), z, workspace=ws,
+                             **kw(act, G, center))
+    check_dict(got, O.group_norm_bwd(f64(c["x"]), f64(c["weight"]), f64(c["bias"]), f64(c["z"]), f64(dy), G, 1e-5, center,
+                                     act))
+    assert (ws[need:] == 77).all()

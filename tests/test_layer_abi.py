@@ -395,3 +395,11 @@ def test_calls_hand_over_every_tensor_they_use(monkeypatch):
          workspace=ws)
     same(ssd.group_norm_fwd, z(*io), z(D), z(D), z(*io), y=z(*io))
     same(ssd.group_norm_bwd, z(*io), z(D), z(D), z(*io), z(*io), workspace=ws)
+
+
+@pytest.mark.parametrize("rows,gs,G", [(1, 8, 2047), (1, 8, 131071), (3, 16, 4099), (2, 8, 7), (5, 264, 601), (1, 1032, 1009)])
+def test_the_norms_workspace_is_bounded_by_the_rows(rows, gs, G):
+    """Two partial sums of 4 bytes for each element of x hold any order of summation; groups whose number
+    shares no factor with the groups of a block do not ask for more."""
+    need = ssd.ssd_group_norm_bwd_workspace_size(norm(rows=rows, channels=gs * G, ngroups=G, z_stride=gs * G))
+    assert 0 < need <= 2 * 4 * rows * gs * G
