@@ -131,11 +131,11 @@ typedef struct {
 
 /* Short causal convolution problem description. */
 typedef struct {
-    int64_t batch;      /* >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
+    int64_t batch;      /* >= 0, <= 2^24; 0 is a no-op (the backward then zeroes its parameter gradients) */
     int64_t seqlen;     /* >= 0, <= 2^30; 0 writes final_state = init_state (or zeros); 1 for ssd_conv1d_update */
     int64_t channels;   /* multiple of 8, <= 2^20 */
     int64_t width;      /* taps: 2, 3 or 4 */
-    int64_t x_stride;   /* elements from a token's row of x to the next: >= channels, multiple of 8 */
+    int64_t x_stride;   /* elements from a token's row of x to the next: >= channels, multiple of 8, <= 2^40 */
     int64_t dx_stride;  /* the same of dx (backward; ignored otherwise) */
     int64_t split1;     /* channels of the second and the third output tensor: multiples of 8, 0 = */
     int64_t split2;     /* no such tensor; the first one has the other channels (at least 8) */
@@ -147,14 +147,14 @@ typedef struct {
 
 /* Selective scan problem description (a decay per channel and state). */
 typedef struct {
-    int64_t batch;      /* >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
+    int64_t batch;      /* >= 0, <= 2^24; 0 is a no-op (the backward then zeroes its parameter gradients) */
     int64_t seqlen;     /* >= 0, <= 2^30; 0 writes final_state = init_state (or zeros); 1 for
                            ssd_selective_state_update */
     int64_t channels;   /* D; channels / ngroups is a multiple of 8; <= 2^20 */
     int64_t dstate;     /* N, multiple of 8, <= 256 */
     int64_t ngroups;    /* G >= 1: channel d uses group d / (D / G) of B and C */
     int64_t z_stride;   /* elements from a token's row of the gate z to the next: >= channels,
-                           multiple of 8 (ignored without z); dz is dense */
+                           multiple of 8, <= 2^40 (ignored without z); dz is dense */
     int32_t io_dtype;   /* dtype of x, dt_raw, B, C, z (backward: also of dy) */
     int32_t y_dtype;    /* dtype of y (backward: of the gradients of the io tensors) */
     int32_t state_dtype;/* dtype of the states */
@@ -162,11 +162,11 @@ typedef struct {
 
 /* Group normalisation problem description. */
 typedef struct {
-    int64_t rows;       /* tokens: >= 0; 0 is a no-op (the backward then zeroes its parameter gradients) */
+    int64_t rows;       /* tokens: >= 0, <= 2^38; 0 is a no-op (the backward then zeroes its parameter gradients) */
     int64_t channels;   /* <= 2^20 */
     int64_t ngroups;    /* channels / ngroups is a multiple of 8, <= 16384 */
-    int64_t z_stride;   /* elements from a row of the gate z to the next: >= channels, multiple of 8
-                           (ignored without z); dz is dense */
+    int64_t z_stride;   /* elements from a row of the gate z to the next: >= channels, multiple of 8,
+                           <= 2^40 (ignored without z); dz is dense */
     float eps;          /* added to the variance: > 0 */
     int32_t x_dtype;    /* dtype of x */
     int32_t io_dtype;   /* dtype of z (backward: also of dy) */
@@ -538,7 +538,9 @@ ssd_status_t ssd_replay_step(const ssd_replay_desc_t* desc, void* checkpoint, vo
  * follow its rule: dy has io_dtype, the gradients of the io tensors y_dtype.
  * SiLU is silu(v) = v / (1 + exp(-v)).  These calls keep no state in the
  * library and use no device memory but their arguments, so calls on different
- * streams may overlap (backward calls: on different workspaces).
+ * streams may overlap (backward calls: on different workspaces).  Beside the
+ * limits at the descriptors, rows x stride above 2^60 and what would take a launch
+ * of 2^31 blocks (both beyond a GPU's memory) are SSD_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------------
  */
 

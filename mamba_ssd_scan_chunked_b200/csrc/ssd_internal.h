@@ -247,8 +247,9 @@ struct SelectiveArgs {
 
 size_t selective_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
 size_t selective_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
-// an upper bound of any of its kernels' blocks
+// blocks of the largest launch, forward or token step, and backward (or a bound of them)
 int64_t selective_blocks(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
+int64_t selective_bwd_blocks(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G);
 cudaError_t launch_selective_fwd(const SelectiveArgs& a, cudaStream_t s);
 cudaError_t launch_selective_update(const SelectiveArgs& a, cudaStream_t s);
 cudaError_t launch_selective_bwd(const SelectiveArgs& a, cudaStream_t s);

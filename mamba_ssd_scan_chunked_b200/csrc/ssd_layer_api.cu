@@ -47,8 +47,13 @@ static size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, size_t e) 
     return rows == 0 ? 0 : ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * e;
 }
 
-constexpr int64_t kMaxChannels = (int64_t)1 << 20, kMaxStride = (int64_t)1 << 24;
+constexpr int64_t kMaxChannels = (int64_t)1 << 20, kMaxStride = (int64_t)1 << 40, kMaxElements = (int64_t)1 << 60;
 constexpr int64_t kMaxBatch = (int64_t)1 << 24, kMaxLen = (int64_t)1 << 30, kMaxBlocks = (int64_t)1 << 31;
+
+// strided rows: offsets and byte counts stay within 64 bits
+static bool rows_fit(int64_t rows, int64_t stride) {
+    return stride <= kMaxStride && (rows == 0 || stride <= kMaxElements / rows);
+}
 
 static ssd_status_t check_conv1d_desc(const ssd_conv1d_desc_t* d, bool backward) {
     if (!d) return SSD_ERR_INVALID_ARG;
@@ -61,11 +66,13 @@ static ssd_status_t check_conv1d_desc(const ssd_conv1d_desc_t* d, bool backward)
         (d->split1 == 0 && d->split2 != 0) || d->x_stride < d->channels || (backward && d->dx_stride < d->channels))
         return SSD_ERR_INVALID_ARG;
     if (d->width < 2 || d->width > 4 || d->channels % 8 || d->split1 % 8 || d->split2 % 8 || d->x_stride % 8 ||
-        d->x_stride > kMaxStride || (backward && (d->dx_stride % 8 || d->dx_stride > kMaxStride)))
+        (backward && d->dx_stride % 8))
         return SSD_ERR_UNSUPPORTED;
     if (d->batch > kMaxBatch || d->seqlen > kMaxLen) return SSD_ERR_UNSUPPORTED;
     if (d->batch * (d->seqlen / 16 + 1) >= kMaxBlocks || conv1d_blocks(d->batch, d->seqlen, d->channels) >= kMaxBlocks)
         return SSD_ERR_UNSUPPORTED;
+    const int64_t rows = d->batch * d->seqlen;
+    if (!rows_fit(rows, d->x_stride) || (backward && !rows_fit(rows, d->dx_stride))) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
@@ -91,12 +98,14 @@ static ssd_status_t check_selective_desc(const ssd_selective_desc_t* d, bool gat
     if (gated && d->z_stride < d->channels) return SSD_ERR_INVALID_ARG;
     if (d->channels > kMaxChannels || (d->channels / d->ngroups) % 8 || d->dstate % 8 || d->dstate > 256)
         return SSD_ERR_UNSUPPORTED;
-    if (gated && (d->z_stride % 8 || d->z_stride > kMaxStride)) return SSD_ERR_UNSUPPORTED;
+    if (gated && d->z_stride % 8) return SSD_ERR_UNSUPPORTED;
     if (d->batch > kMaxBatch || d->seqlen > kMaxLen || d->batch * (d->seqlen / 8 + 1) >= kMaxBlocks)
         return SSD_ERR_UNSUPPORTED;
     if (d->batch * (d->seqlen / 8 + 1) * d->ngroups >= kMaxBlocks ||
-        selective_blocks(d->batch, d->seqlen, d->channels, d->dstate, d->ngroups) >= kMaxBlocks / 2)
+        selective_blocks(d->batch, d->seqlen, d->channels, d->dstate, d->ngroups) >= kMaxBlocks ||
+        selective_bwd_blocks(d->batch, d->seqlen, d->channels, d->dstate, d->ngroups) >= kMaxBlocks)
         return SSD_ERR_UNSUPPORTED;
+    if (gated && !rows_fit(d->batch * d->seqlen, d->z_stride)) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
@@ -118,8 +127,8 @@ static ssd_status_t check_norm_desc(const ssd_group_norm_desc_t* d) {
     if (gated && d->z_stride < d->channels) return SSD_ERR_INVALID_ARG;
     const int64_t gs = d->channels / d->ngroups;
     if (d->channels > kMaxChannels || gs % 8 || gs > 16384) return SSD_ERR_UNSUPPORTED;
-    if (gated && (d->z_stride % 8 || d->z_stride > kMaxStride)) return SSD_ERR_UNSUPPORTED;
-    if (d->rows > ((int64_t)1 << 38)) return SSD_ERR_UNSUPPORTED;
+    if (gated && d->z_stride % 8) return SSD_ERR_UNSUPPORTED;
+    if (d->rows > ((int64_t)1 << 38) || (gated && !rows_fit(d->rows, d->z_stride))) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

@@ -448,8 +448,11 @@ size_t selective_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64
     return chunk_state_bytes(batch, D, N, sh.nch) + (size_t)batch * (sh.nch - 1) * D * sizeof(float);
 }
 
-int64_t selective_blocks(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t) {
-    return batch * (L / 8 + 1) * (D / 8) * ((N + 15) / 16);
+int64_t selective_blocks(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
+    const SelShape sh = sel_shape(batch, L, D, N, G);
+    const int64_t walk = batch * G * sh.tiles * (sh.nch > 1 ? sh.nch - 1 : 1);
+    const int64_t join = sh.nch > 1 ? (batch * D * N + 127) / 128 : 0, token = batch * ((D + 3) / 4);   // K <= 32
+    return walk > join ? (walk > token ? walk : token) : (join > token ? join : token);
 }
 
 template <typename IoT, typename YT, class Tile, int T>

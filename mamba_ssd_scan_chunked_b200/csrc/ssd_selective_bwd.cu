@@ -88,6 +88,13 @@ size_t selective_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, i
     return batch == 0 || L == 0 ? 0 : sb_shape(batch, L, D, N, G).total;
 }
 
+int64_t selective_bwd_blocks(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
+    const SbShape sh = sb_shape(batch, L, D, N, G);
+    const int64_t walk = batch * sh.nch * G * sh.tiles, join = 2 * ((batch * D * N + 127) / 128);
+    const int64_t sums = (2 * batch * L * G * N + 31) / 32 + (D * N + 31) / 32 + (2 * D + 31) / 32;
+    return walk > join ? (walk > sums ? walk : sums) : (join > sums ? join : sums);
+}
+
 // B and C of a chunk in fp32, zero past the sequence
 template <typename IoT, int T, int Np, int THREADS>
 __device__ __forceinline__ void stage_bc(const SelectiveArgs& a, int64_t b, int64_t g, int64_t t0, int nt, float* sB,

@@ -403,3 +403,41 @@ def test_the_norms_workspace_is_bounded_by_the_rows(rows, gs, G):
     shares no factor with the groups of a block do not ask for more."""
     need = ssd.ssd_group_norm_bwd_workspace_size(norm(rows=rows, channels=gs * G, ngroups=G, z_stride=gs * G))
     assert 0 < need <= 2 * 4 * rows * gs * G
+
+
+ROW = 8192 * 8512          # from the last token of a prompt's rows to the next sequence's
+
+
+def test_rows_far_apart_are_taken():
+    """The last tokens of a prompt's rows, or one column block of very long ones, are strided rows like others."""
+    upd, _ = caller(ssd.ssd_conv1d_update, CONV_UPD, ("bias", "y1", "y2"), {})
+    assert upd(conv(batch=0, seqlen=1, x_stride=ROW), state=0, x=0, y0=0) == OK
+    fwd, _ = caller(ssd.ssd_conv1d_fwd, CONV_FWD, ("bias", "init_state", "pad_left", "y1", "y2", "final_state"), {})
+    assert fwd(conv(batch=0, x_stride=ROW), x=0, y0=0) == OK
+    assert ssd.ssd_conv1d_bwd_workspace_size(conv(x_stride=ROW, dx_stride=1 << 40)) > 0
+    step, _ = caller(ssd.ssd_selective_state_update, ("state",) + SEL_IN + ("y",), ("dt_bias", "D"), {})
+    assert step(sel(seqlen=1, batch=0, z_stride=ROW), state=0, x=0, dt_raw=0, B=0, C=0, y=0) == OK
+    gn, _ = caller(ssd.ssd_group_norm_fwd, ("x", "z", "weight", "bias", "y"), ("weight", "bias"), {})
+    assert gn(norm(rows=0, z_stride=ROW), x=0, z=0, y=0) == OK
+
+
+@pytest.mark.parametrize("far", [(1 << 40) + 8, 1 << 62])
+def test_rows_beyond_any_memory_are_refused(far):
+    upd, _ = caller(ssd.ssd_conv1d_update, CONV_UPD, ("bias", "y1", "y2"), {})
+    assert upd(conv(seqlen=1, x_stride=far)) == UNSUPPORTED
+    step, _ = caller(ssd.ssd_selective_state_update, ("state",) + SEL_IN + ("y",), ("dt_bias", "D"), {})
+    assert step(sel(seqlen=1, z_stride=far)) == UNSUPPORTED
+    for make in (lambda: ssd.ssd_conv1d_bwd_workspace_size(conv(dx_stride=far)),
+                 lambda: ssd.ssd_conv1d_bwd_workspace_size(conv(batch=1 << 20, seqlen=2, x_stride=1 << 40)),
+                 lambda: ssd.ssd_group_norm_bwd_workspace_size(norm(z_stride=far)),
+                 lambda: ssd.ssd_group_norm_bwd_workspace_size(norm(rows=1 << 21, z_stride=1 << 40))):
+        with pytest.raises(ssd.SsdError) as e:
+            make()
+        assert e.value.status == UNSUPPORTED
+
+
+@pytest.mark.parametrize("batch,L,D,N", [(64, 8192, 8192, 256), (128, 8192, 8192, 128), (256, 1, 8192, 256),
+                                         (1, 1 << 20, 8192, 256)])
+def test_large_selective_scans_are_taken(batch, L, D, N):
+    """x of 17 GB at most: the scan's tensors fit a GPU's memory, and its grids are far below 2^31 blocks."""
+    ssd.ssd_selective_scan_workspace_size(sel(batch=batch, seqlen=L, channels=D, dstate=N, ngroups=1))

@@ -309,3 +309,62 @@ def test_calls_without_the_optional_gradients():
     a = ssd.group_norm_bwd(x, one, zero, dy, ngroups=3)
     b = ssd.group_norm_bwd(x, None, None, dy, ngroups=3)
     assert b["dweight"] is None and b["dbias"] is None and t.equal(a["dx"], b["dx"])
+
+
+def test_the_last_tokens_of_long_rows_as_a_steps_inputs():
+    """x and z of a token step cut out of a prompt's rows without a copy: 2^24 and more elements from one
+    sequence to the next."""
+    t = torch()
+    b, L, D, N = 3, 2049, 72, 16
+    c = selective(95, b, 1, D, N)
+    d = {k: to_dev(v) for k, v in c.items()}
+    rows = t.full((b, L, 8200), float("nan"), device="cuda")
+    rows[:, -1, :2 * D] = d["row"][:, 0]
+    x, z = rows[:, -1, :D], rows[:, -1, D:2 * D]
+    assert x.stride(0) > 1 << 24
+    kept, state = t.randn(b, 3, D, device="cuda"), t.randn(b, D, N, device="cuda")
+    par = [d["dt_raw"][:, 0].contiguous(), d["dt_bias"], d["A"], d["B"][:, 0].contiguous(), d["C"][:, 0].contiguous(), d["D"]]
+    outs = []
+    for xs, zs in ((x, z), (x.contiguous(), z.contiguous())):
+        k, h = kept.clone(), state.clone()
+        v = ssd.conv1d_update(k, xs, d["w"], d["bias"])
+        y = ssd.selective_state_update(h, v, *par, zs)
+        outs.append((k, v, h, y, ssd.group_norm_fwd(y, None, None, zs, ngroups=3)))
+        assert all(o.isfinite().all() for o in outs[-1])
+    assert all(t.equal(a, b) for a, b in zip(*outs))
+
+
+def test_a_convolution_and_a_norm_past_32_bits():
+    """2^32 elements and more of x and y (bf16, 8.6 GB each): the last tokens as a call of their own gives them."""
+    t = torch()
+    b, L, D = 2, (1 << 18) + 37, 8200
+    assert b * L * D > 1 << 32
+    gen = t.Generator("cuda").manual_seed(3)
+    x = t.empty(b, L, D, dtype=t.bfloat16, device="cuda").normal_(generator=gen)
+    w, bias = t.randn(D, 4, device="cuda", generator=gen), t.randn(D, device="cuda", generator=gen)
+    y, kept = ssd.conv1d_fwd(x, w, bias)
+    tail = x[1:, -40:].contiguous()
+    want, wkept = ssd.conv1d_fwd(tail, w, bias, x[1:, -43:-40].float().contiguous())
+    assert t.equal(y[1:, -40:], want) and t.equal(kept[1:], wkept)
+    g = ssd.conv1d_bwd(x, w, bias, y)["dx"]
+    own = ssd.conv1d_bwd(tail, w, bias, want, x[1:, -43:-40].float().contiguous())["dx"]
+    assert t.equal(g[1:, -40:], own)
+    del g
+    n = ssd.group_norm_fwd(x, bias, None, y, ngroups=5, y=t.empty_like(x))
+    assert t.equal(n[1:, -40:], ssd.group_norm_fwd(tail, bias, None, want, ngroups=5))
+
+
+def test_a_selective_scan_past_32_bits():
+    """64 x 8192 tokens x 8192 channels, 256 states: 2^32 elements of x, dt and y, the same sequence in every
+    place of the batch."""
+    t = torch()
+    b, L, D, N = 64, 8192, 8192, 256
+    gen = t.Generator("cuda").manual_seed(4)
+    one = lambda *s: t.empty(s, dtype=t.bfloat16, device="cuda").normal_(generator=gen)
+    x, dt, B, C = one(1, L, D), one(1, L, D), one(1, L, 1, N), one(1, L, 1, N)
+    A = -t.rand(D, N, device="cuda", generator=gen) - 0.1
+    want, state = ssd.selective_scan_fwd(x, dt, None, A, B, C, None)
+    y, final = ssd.selective_scan_fwd(*(v.expand(b, *v.shape[1:]).contiguous() for v in (x, dt)), None, A,
+                                      *(v.expand(b, *v.shape[1:]).contiguous() for v in (B, C)), None)
+    for i in (0, 31, 63):
+        assert t.equal(y[i], want[0]) and t.equal(final[i], state[0])
