@@ -117,3 +117,70 @@ def test_conv1d_bwd_repeats_bit_for_bit():
     outs = [ssd.conv1d_bwd(dev(c["x"]), dev(c["weight"]), dev(c["bias"]), dy, dev(c["init"])) for _ in range(2)]
     for k in outs[0]:
         assert t.equal(outs[0][k], outs[1][k]), k
+
+
+@pytest.mark.parametrize("b,L,split,W,io,y,state,init,pad,extra", [
+    (4, 613, (4104,), 4, F, F, F, True, [1, 31, 33, 613], 0),          # padding beside a run's border, and all of it
+    (4, 613, (4104,), 3, F, F, F, True, [64, 612, 0, 611], 8),
+    (3, 805, (4096, 128, 128), 4, B, B, F, False, None, 24),            # x, B, C out of wider rows
+    (2, 1281, (4104,), 2, B, F, B, True, None, 0),                      # one token into the last run
+])
+def test_conv1d_fwd_in_runs_of_32_tokens(b, L, split, W, io, y, state, init, pad, extra):
+    """As many channels and tokens as take the long runs (75776 threads with runs of 32)."""
+    t = torch()
+    D = sum(split)
+    assert b * -(-L // 32) * (D // 4) >= 148 * 512
+    c = case(b, L, D, W, io, state, init, True, 110 + L + W)
+    x = rows_of(c["x"], extra)
+    if pad is not None:
+        for i, p in enumerate(pad):
+            x[i, :p] = float("nan") if i % 2 else float("inf")
+    got, final = ssd.conv1d_fwd(x, dev(c["weight"]), dev(c["bias"]), dev(c["init"]), split=split, y_dtype=t_dtype(y),
+                                state_dtype=t_dtype(state),
+                                pad_left=None if pad is None else t.tensor(pad, dtype=t.int32, device="cuda"))
+    ref, fref = O.conv1d(f64(c["x"]), f64(c["weight"]), f64(c["bias"]), f64(c["init"]), pad, True)
+    for i, (g, r) in enumerate(zip(got, pieces(ref, split))):
+        check(f"y{i}", g, r)
+    check("final", final, fref)
+    if pad is not None:
+        for i, p in enumerate(pad):
+            assert not got[0][i, :p].any()
+
+
+@pytest.mark.parametrize("run,b,L,split,W,io,g,extra", [
+    (32, 4, 287, (8200,), 4, F, F, 0),                                  # one token short of the last warp's run
+    (32, 3, 353, (8064, 64, 72), 3, B, B, 8),                           # one into it
+    (64, 4, 449, (8200,), 4, B, F, 0),
+    (64, 4, 511, (8064, 64, 72), 2, F, F, 16),
+    (128, 4, 895, (8200,), 4, F, F, 0),
+    (128, 4, 897, (8064, 64, 72), 4, B, B, 24),
+])
+def test_conv1d_bwd_in_runs_of_more_tokens(run, b, L, split, W, io, g, extra):
+    """The runs of 32, 64 and 128 tokens a warp, with kept inputs and their gradients; which one a size takes shows
+    in the workspace, a row of sums for each four runs."""
+    t = torch()
+    D = sum(split)
+    c = case(b, L, D, W, io, F, True, True, 310 + L)
+    need = ssd.ssd_conv1d_bwd_workspace_size(ssd.Conv1dDesc(b, L, D, W, D + extra, D + extra, 0, 0, 0, 0, 0, 1))
+    assert need == 4 * D * (W + 1) * b * -(-L // (4 * run))
+    dy, df = draw([17, L], (b, L, D), io), draw([18, L], (b, W - 1, D), F)
+    dx = t.full((b, L, D + extra), 7.0, dtype=t_dtype(g), device="cuda")
+    dys = tuple(to_dev(np.ascontiguousarray(p)) for p in pieces(dy, split))
+    call = lambda: ssd.conv1d_bwd(rows_of(c["x"], extra), dev(c["weight"]), dev(c["bias"]), dys, dev(c["init"]), dev(df),
+                                  dx=dx[..., extra:])
+    got = call()
+    check_dict(got, O.conv1d_bwd(f64(c["x"]), f64(c["weight"]), f64(c["bias"]), f64(c["init"]), f64(dy), f64(df)))
+    assert (dx[..., :extra] == 7.0).all()
+    first = {k: v.clone() for k, v in got.items()}
+    again = call()
+    assert all(t.equal(again[k], first[k]) for k in first)
+
+
+@pytest.mark.parametrize("b,D,W", [(3, 72, 4), (650, 1160, 3), (5, 16, 2)])
+def test_conv1d_update_of_a_bf16_state_and_fp32_inputs(b, D, W):
+    """y reads the token as it is; the state keeps it rounded once."""
+    c = case(b, 1, D, W, F, B, True, True, 210 + D)
+    ref, fref = O.conv1d(f64(c["x"]), f64(c["weight"]), f64(c["bias"]), f64(c["init"]))
+    st = to_dev(c["init"])
+    check("y", ssd.conv1d_update(st, dev(c["x"])[:, 0], dev(c["weight"]), dev(c["bias"])), ref[:, 0])
+    check("state", st, fref)
