@@ -121,3 +121,33 @@ def test_few_rows_of_many_groups(rows, gs, G, center, act):
     check_dict(got, O.group_norm_bwd(f64(c["x"]), f64(c["weight"]), f64(c["bias"]), f64(c["z"]), f64(dy), G, 1e-5, center,
                                      act))
     assert (ws[need:] == 77).all()
+
+
+@pytest.mark.parametrize("rows,gs,G,x,io,y,center,act,bias,extra", [
+    (12001, 64, 3, F, B, B, False, "before", True, 8),                  # 32 slots a block
+    (40001, 8, 5, F, F, F, True, "after", True, 0),                     # 256 slots a block
+    (2003, 256, 5, B, B, F, True, "silu", True, 0),                     # a warp a slot
+    (2001, 264, 3, F, F, F, False, "before", False, 24),                # several slots of two warps
+    (701, 1032, 3, B, F, B, True, "after", True, 8),
+    (1501, 4096, 1, F, B, B, False, "before", True, 40),                # a slot a block
+    (503, 8192, 1, F, F, F, True, "after", True, 16),                   # two vectors a lane backward
+    (499, 8192, 2, B, B, B, False, "before", True, 8),
+    (501, 16384, 1, F, F, F, False, "before", True, 8),
+])
+def test_slots_of_several_rows(rows, gs, G, x, io, y, center, act, bias, extra):
+    """A slot walks over rows: the steps of x and of the gate's wider rows, the exchange's two halves in turn and
+    the sums of dw and db over a slot's rows.  The backward's partial sums tell the slots; the forward has twice
+    as many at most."""
+    C = gs * G
+    parts = ssd.ssd_group_norm_bwd_workspace_size(ssd.GroupNormDesc(rows, C, G, C + extra, 1e-5, 0, 0, 0, 0, 3)) // (8 * C)
+    assert 2 * parts < rows and rows % parts
+    c = inputs(rows, C, x, io, act, True, bias, 720 + gs)
+    z, dy = None if c["z"] is None else rows_of(c["z"], extra), draw([19, gs], (rows, C), io)
+    f = {k: f64(v) for k, v in c.items()}
+    got = ssd.group_norm_fwd(dev(c["x"]), dev(c["weight"]), dev(c["bias"]), z, y_dtype=t_dtype(y), **kw(act, G, center))
+    check("y", got, O.group_norm(f["x"], f["weight"], f["bias"], f["z"], G, 1e-5, center, act))
+    got = ssd.group_norm_bwd(dev(c["x"]), dev(c["weight"]), dev(c["bias"]), to_dev(dy), z, grad_dtype=t_dtype(y),
+                             **kw(act, G, center))
+    ref = O.group_norm_bwd(f["x"], f["weight"], f["bias"], f["z"], f64(dy), G, 1e-5, center, act)
+    ref["dbias"] = ref["dbias"] if bias else None
+    check_dict(got, ref)
