@@ -219,3 +219,65 @@ def test_a_token_step_of_a_state_that_forgets_at_once():
     h, y = O.selective_step(f["init"], f["x"], f["dt_raw"], f["dt_bias"], f["A"], f["B"], f["C"], f["D"], f["z"])
     check("y", ssd.selective_state_update(d["init"], *args(d), d["z"]), y)
     check("state", d["init"], h)
+
+
+@pytest.mark.parametrize("b,D,N,G,io,gate", [
+    (475, 264, 8, 1, F, True),                                          # two lanes a channel
+    (301, 264, 16, 1, B, True),                                         # four, too few sequences for four a thread
+    (91, 528, 24, 2, F, False),
+])
+def test_token_steps_of_two_sequences_a_thread(b, D, N, G, io, gate):
+    """The token step's middle form: fp32 states whose two sequences a thread fill the machine (1184 blocks) and
+    whose four do not, or whose lanes are two."""
+    K = 1 << (N // 4 - 1).bit_length()
+    blocks = lambda n: -(-b // n) * -(-D // (128 // K))
+    assert blocks(2) >= 148 * 8 and (K < 4 or blocks(4) < 148 * 8)
+    c = case(b, None, D, N, G, io, F, True, gate, True, 510 + D + N)
+    d, f = on_gpu(c, 8), {k: f64(v) for k, v in c.items()}
+    h, y = O.selective_step(f["init"], f["x"], f["dt_raw"], f["dt_bias"], f["A"], f["B"], f["C"], f["D"], f["z"])
+    check("y", ssd.selective_state_update(d["init"], *args(d), d["z"]), y)
+    check("state", d["init"], h)
+
+
+@pytest.mark.parametrize("b,L,D,N,G,io,pad", [
+    (1, 700, 24, 128, 1, F, None),
+    (2, 697, 16, 128, 2, F, [0, 333]),
+    (1, 500, 24, 200, 1, F, None),                                      # tiles of 16 tokens
+    (2, 333, 16, 256, 1, F, [332, 17]),
+    (1, 701, 40, 72, 1, B, [129]),
+])
+def test_cut_sequences_of_many_states(b, L, D, N, G, io, pad):
+    """More than 64 states in chunks: the summaries of a warp of states a channel."""
+    t = torch()
+    assert ssd.ssd_selective_scan_workspace_size(ssd.SelectiveDesc(b, L, D, N, G, D, 0, 0, 0)) > 0
+    c = case(b, L, D, N, G, io, F, True, True, True, 410 + L + N)
+    c["A"] /= 16                                                        # decays that carry from chunk to chunk
+    d, f = on_gpu(c, 8), {k: f64(v) for k, v in c.items()}
+    if pad is not None:
+        for i, p in enumerate(pad):
+            for k in ("x", "dt_raw", "B", "C", "z"):
+                d[k][i, :p] = float("nan") if i % 2 else float("inf")
+    y, final = ssd.selective_scan_fwd(*args(d), d["z"], d["init"], y_dtype=t.float32,
+                                      pad_left=None if pad is None else t.tensor(pad, dtype=t.int32, device="cuda"))
+    ref, fref = O.selective_scan(*args(f), f["z"], f["init"], pad)
+    check("y", y, ref)
+    check("final", final, fref)
+
+
+def test_dt_keeps_its_relative_precision():
+    """y = dt where A = 0, x = B = C = 1 of one state: softplus over five decades of dt below 1, around 0 and above.
+    The exponential is off by 2^-22 of itself, the polynomial by 2^-23 with its roundings, the sum by 2^-24 and
+    dt_raw + dt_bias, exact here, by nothing: 2^-22 + 2^-23 + 2^-24 < 4.2e-7 of dt."""
+    t = torch()
+    raw = np.concatenate([np.linspace(-80, 30, 4000), np.linspace(-2, 2, 4000), [0.0, -1e-8, 1e-8]]).astype(np.float32)
+    raw = np.pad(raw, (0, -len(raw) % 8))
+    n = len(raw)
+    one, B = t.ones(1, 1, n, device="cuda"), t.zeros(1, 1, 1, 8, device="cuda")
+    B[..., 0] = 1.0
+    A = t.zeros(n, 8, device="cuda")
+    want = O.softplus(raw.astype(np.float64))
+    y, _ = ssd.selective_scan_fwd(one, to_dev(raw)[None, None], None, A, B, B, None)
+    step = ssd.selective_state_update(t.zeros(1, n, 8, device="cuda"), one[:, 0], to_dev(raw)[None], None, A, B[:, 0],
+                                      B[:, 0], None)
+    for got in (y[0, 0], step[0]):
+        assert (np.abs(got.double().cpu().numpy() - want) <= 4.2e-7 * want).all()
