@@ -261,7 +261,8 @@ __device__ __forceinline__ void selective_walk(const SelectiveArgs& a, const Sel
 }
 
 // DEEP: for blocks of 4 warps of which an SM has two at most, registers for two
-// rounds side by side (4 x 2048 x 4096: 246 -> 232 us; three blocks an SM lose by it)
+// rounds side by side (4 x 2048 x 4096: 245 us with one round in the registers of
+// three blocks an SM, 248 us with two rounds in them, 232 us with two in those of two)
 template <typename IoT, typename YT, class Tile, int T, bool FIRST, bool DEEP>
 __global__ void __launch_bounds__(Tile::W * 32, Tile::W == 4 && !DEEP ? 3 : Tile::W <= 8 ? 2 : 1)
 selective_fwd_kernel(const SelectiveArgs a, const SelShape sh, float* __restrict__ wstate, float* __restrict__ wdt) {
@@ -401,17 +402,24 @@ selective_update_kernel(const SelectiveArgs a, int K, int cblocks, int Dg) {
 // Tiles by the number of states: 8 states a lane from 9 to 32 states and beyond 128
 // (half the loads and sums of 4 for each state: 246 against 251 us at 4 x 2048 x
 // 4096, state 16, with half the warps), 4 otherwise; more warps a block where a warp
-// covers few channels, so that a token's row stays whole vectors.
+// covers few channels, so that a token's row stays whole vectors.  Of 33 to 128 states
+// 4 a lane is the slower side, at 4 x 2048 tokens x 2048 channels, bf16, gated: 64
+// states 443 us against 425 with 8 a lane and half the warps, 128 states 1039 us
+// against 855.  8 states 200 us (4096 channels), 256 states 1438 us (2 x 2048 x 2048).
 constexpr int kSelMaxChunks = 64;
 
 static int tile_channels(int64_t N) { return N <= 8 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 static int tile_tokens(int64_t N) { return N > 128 ? 16 : 32; }
 
-// Three blocks an SM saturate it.  Cutting the sequence costs a second exponential
-// per state and token, so it pays once the two launches of nch - 1 chunks are of four
-// chunks or more: from 100 blocks down (1 x 16384 tokens, 2048 channels, state 16: 32
-// blocks; 6311 us in one chunk by the first kernel, 372 us in 14 by this one; 3 x 777
-// x 520 fp32, state 24: 39 us in 9, 43 us in 6).
+// Cutting the sequence costs a second exponential per state and token, and pays while
+// there are blocks for two SMs in three at most: from 100 blocks down, into as many
+// chunks as make three blocks an SM.  Cut against whole, bf16, gated, state 16:
+// 1 x 16384 tokens, 32 blocks 372 and 1179 us; 1 x 4096 tokens, 64 blocks 192 and 299
+// us, 80 blocks 228 and 299, 100 blocks 267 and 299, 128 blocks 334 and 300.  Four
+// chunks (three a launch) at least: 1 x 256 tokens, 32 blocks, 22.9 and 22.7 us in
+// four, 1 x 512 tokens 28.5 and 41.0 us in eight; a short sequence of many channels
+// loses by it (1 x 320 tokens, 100 blocks: 36.7 and 27.6 us).  3 x 777 x 520 fp32,
+// state 24: 38 and 52 us.
 static SelShape sel_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
     SelShape sh{};
     const int CT = tile_channels(N), T = tile_tokens(N);

@@ -368,3 +368,26 @@ def test_a_selective_scan_past_32_bits():
                                       *(v.expand(b, *v.shape[1:]).contiguous() for v in (B, C)), None)
     for i in (0, 31, 63):
         assert t.equal(y[i], want[0]) and t.equal(final[i], state[0])
+
+
+def test_a_given_stream_inside_a_captured_fork():
+    """A capture forked to the given stream: the wait becomes an edge of the graph, and replays repeat the result."""
+    t = torch()
+    d = {k: to_dev(v) for k, v in selective(96).items()}
+    x, z = d["row"][..., :72], d["row"][..., 72:]
+    want, kept = ssd.conv1d_fwd(x, d["w"], d["bias"])
+    gated = ssd.group_norm_fwd(want, None, None, z, ngroups=3)
+    side, graph = t.cuda.Stream(), t.cuda.CUDAGraph()
+    t.cuda.synchronize()
+    with t.cuda.graph(graph):
+        main = t.cuda.current_stream()
+        side.wait_stream(main)
+        y, k = ssd.conv1d_fwd(x, d["w"], d["bias"], stream=side)
+        n = ssd.group_norm_fwd(y, None, None, z, ngroups=3, stream=side)
+        main.wait_stream(side)
+    for _ in range(2):
+        for v in (y, k, n):
+            v.zero_()
+        graph.replay()
+        t.cuda.synchronize()
+        assert t.equal(y, want) and t.equal(k, kept) and t.equal(n, gated)
