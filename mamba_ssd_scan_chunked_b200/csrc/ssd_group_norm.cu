@@ -40,8 +40,13 @@ struct NormShape {
     int threads;     // of a block
     int per_block;   // slots of a block
     int64_t blocks, items;
-    int64_t parts;   // rows of the backward's partial sums
 };
+
+// rows of the backward's partial sums: of the slots, or of x where a slot has one item at most
+__host__ __device__ __forceinline__ int64_t norm_parts(const NormShape& sh, int64_t rows, int64_t G) {
+    const int64_t slots = sh.blocks * sh.per_block;
+    return slots < sh.items ? slots / G : rows;
+}
 
 // Where a thread stands, and its way through the sums over its slot: within a
 // warp, then, across the slot's warps, through shared memory, whose two halves take
@@ -371,10 +376,10 @@ group_norm_bwd_kernel(const GroupNormArgs a, const NormShape sh) {
         dxp += xstep;
         dzp += xstep;
     }
-    // slot q's sums: row q / G of [parts][C]
+    // slot q's sums: row q / G of [norm_parts][C]
     if (at.first >= sh.items) return;
     float* part = a.ws + at.first * sh.gs;
-    const int64_t all = sh.parts * a.C;
+    const int64_t all = norm_parts(sh, a.rows, a.G) * a.C;
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
         const int i = (at.lane + q * sh.lanes) * 8;
@@ -423,16 +428,14 @@ static NormShape norm_shape(int64_t rows, int64_t C, int64_t G, bool backward, N
     const int64_t unit = G / x, want = (sh.items + sh.per_block - 1) / sh.per_block;
     const bool half = *cls == NormClass::kBlock512 || (backward && *cls == NormClass::kBlock1024);
     const int64_t most = (int64_t)148 * norm_blocks_per_sm(backward, *cls == NormClass::kWarp ? 256 : half ? 512 : 1024);
-    const bool single = want < most || want <= unit;
-    sh.blocks = single ? want : most / unit > 0 ? most / unit * unit : unit;
-    sh.parts = single ? rows : sh.blocks * sh.per_block / G;
+    sh.blocks = want < most || want <= unit ? want : most / unit > 0 ? most / unit * unit : unit;
     return sh;
 }
 
 size_t group_norm_bwd_workspace(int64_t rows, int64_t C, int64_t G) {
     NormClass cls;
     const NormShape sh = norm_shape(rows, C, G, true, &cls);
-    return (size_t)sh.parts * C * 2 * sizeof(float);
+    return (size_t)norm_parts(sh, rows, G) * C * 2 * sizeof(float);
 }
 
 template <typename X, typename I, typename Y> struct NormFwd {
@@ -483,8 +486,9 @@ cudaError_t launch_group_norm_bwd(const GroupNormArgs& a, cudaStream_t s) {
     dispatch_types<NormBwd>(a, sh, cls, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!a.dw && !a.db)) return e;
-    const ColumnSum sums[] = {{a.ws, sh.parts, a.C, a.dw ? a.C : 0, a.dw, a.C, nullptr, false},
-                              {a.ws + sh.parts * a.C, sh.parts, a.C, a.db ? a.C : 0, a.db, a.C, nullptr, false}};
+    const int64_t parts = norm_parts(sh, a.rows, a.G);
+    const ColumnSum sums[] = {{a.ws, parts, a.C, a.dw ? a.C : 0, a.dw, a.C, nullptr, false},
+                              {a.ws + parts * a.C, parts, a.C, a.db ? a.C : 0, a.db, a.C, nullptr, false}};
     return launch_column_sums(sums, 2, s);
 }
 
